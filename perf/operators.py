@@ -99,6 +99,9 @@ def draw(rng):
     n = min(rng.choice([1, 2, 3, 5, 8, 13, 32]), total)
     cuts = sorted(rng.randint(0, total) for _ in range(n - 1))
     lens = [b - a for a, b in zip([0] + cuts, cuts + [total])]
+    if kind == "train" and max(lens) < 2:
+        # a token alone in its sequence has no gradient of q and k: one pair of tokens at least
+        lens = [max(total, 2)]
     return _attention(kind, lens, kv * group, kv, dim, causal, dtype, fused)
 
 
