@@ -81,7 +81,9 @@ enum {
   PACK3D_ERR_COORDS = -2,      /* coordinates out of range or not a bijection */
   PACK3D_ERR_CUDA = -3,        /* a CUDA launch or runtime call failed */
   PACK3D_ERR_TIMEOUT = -4,     /* a bounded device-side wait gave up */
-  PACK3D_ERR_UNSUPPORTED = -5  /* valid operator, shape not built into this library */
+  PACK3D_ERR_UNSUPPORTED = -5, /* valid operator, shape not built into this library */
+  PACK3D_ERR_LENGTHS = -6      /* prefix sums of a pack's lengths that do not start at 0, fall, or
+                                  end behind the tensors */
 };
 
 /* Operator shape and conventions.  head_dim must be a multiple of 12 and at
@@ -367,6 +369,167 @@ PACK3D_API int pack3d_wait_selftest(uint32_t polls, pack3d_stream_t stream);
 
 /* Human-readable text of a status code (static storage). */
 PACK3D_API const char* pack3d_strerror(int status);
+
+/* ---- packed sequences ------------------------------------------------------
+ *
+ * Dense attention over sequences of different lengths packed one behind the
+ * other, and rotary positions: what a model needs beside the local-global
+ * operator where several volumes or sequences share one pack and every token
+ * attends to all (or, causal, to all earlier) tokens of its own sequence.
+ *
+ * Sequence s holds the rows [cu[s], cu[s + 1]) of the packed tensors, cu the
+ * prefix sums of the lengths (cu[0] = 0; a length may be 0).  Rows behind
+ * cu[n_seqs] belong to no sequence: they are read nowhere and written nowhere.
+ * Query head h uses key/value head h / (Hq / Hk).  With P the softmax over the
+ * row's own sequence (its tokens up to and including itself when causal):
+ *
+ *   S_ij = scale q_i . k_j,  lse_i = ln sum_j exp S_ij,  out_i = sum_j P_ij v_j
+ *
+ * Every row of a sequence sees at least itself, so no row is empty.
+ *
+ * Layouts: q, out, dout, dq [n_tokens][Hq][head_dim] and k, v, dk, dv
+ * [n_tokens][Hk][head_dim] of dtype, heads side by side, tokens
+ * pack3d_seq_strides apart (so q, k and v may be slices of one projection's
+ * output); lse fp32 [Hq][n_tokens].  PACK3D_BF16 runs on the tensor cores
+ * (products accumulated in fp32, the softmax weights and their gradients rounded
+ * to bf16 as the operands of the next product), PACK3D_FP32 on the CUDA cores in
+ * fp32 throughout.  Results do not depend on the run: no atomics enter a sum.
+ *
+ * Non-finite values: what stands in another sequence or behind the last one
+ * never reaches a row.  Inside a causal sequence a non-finite value, gradient
+ * or query of a token may also reach rows of up to 256 tokens before it (a
+ * masked weight of zero times that value). */
+
+/* head_dim a multiple of 8, 8 .. 128; Hq a multiple of Hk; 1 <= n_seqs,
+ * 0 <= n_tokens <= 2^30; Hq <= 65535. */
+typedef struct {
+  int32_t n_seqs;
+  int32_t n_tokens; /* rows of the packed tensors (cu[n_seqs] may be smaller) */
+  int32_t Hq, Hk, head_dim;
+  int32_t causal;   /* nonzero: token i sees the tokens of its sequence up to itself */
+  float scale;      /* softmax scale; <= 0 selects 1 / sqrt(head_dim) */
+  int32_t dtype;    /* PACK3D_BF16 or PACK3D_FP32 */
+} pack3d_seq_params;
+
+/* Elements between two tokens of each tensor; 0 (or a NULL struct) for tensors
+ * without gaps.  At least heads * head_dim, multiples of 8; every tensor
+ * starts on a 16-byte boundary. */
+typedef struct {
+  int64_t q, k, v, out, dout, dq, dk, dv;
+} pack3d_seq_strides;
+
+/* Index of a pack, built by pack3d_seq_build_index into one caller-allocated
+ * device buffer (see pack3d_seq_index_init).
+ *   pos   int32 [n_tokens]  position in its sequence, -1 behind the last one
+ *                           (the positions pack3d_rotary takes)
+ *   seq   int32 [n_tokens]  number of the row's sequence, -1 behind the last one
+ *   pair, query, key        int32 [n][4] tile lists (first row of the sequence, its
+ *                           length, first row of the tile in it, 0), the
+ *                           costliest tiles first: 256-row query tiles,
+ *                           128-row query tiles, 128-row key tiles
+ *   err   int32 [2]         [0]: 0 or a bit set of 1 = bad lengths, 4 = a kernel
+ *                           gave up a bounded device-side wait
+ */
+typedef struct {
+  int32_t* pos;
+  int32_t* seq;
+  int32_t* pair;
+  int32_t* query;
+  int32_t* key;
+  int32_t* err;
+  int32_t n_pair, n_rows; /* entries of pair; of query and of key (some unused) */
+} pack3d_seq_index;
+
+/* Bytes of device memory an index needs (0 if the params are invalid).
+ * Host-only; no CUDA call. */
+PACK3D_API size_t pack3d_seq_index_bytes(const pack3d_seq_params* p);
+
+/* Carve an index out of a caller-allocated device buffer of at least
+ * pack3d_seq_index_bytes(p) bytes, aligned to 256 bytes.  Fills *out; no CUDA
+ * call. */
+PACK3D_API int pack3d_seq_index_init(const pack3d_seq_params* p, void* buffer, size_t bytes,
+                                     pack3d_seq_index* out);
+
+/* Build the index from the prefix sums (int32 [n_seqs + 1], device).
+ * Asynchronous: bad lengths are recorded in idx->err on the device and make
+ * every later attention call with this index return without writing. */
+PACK3D_API int pack3d_seq_build_index(const pack3d_seq_params* p, const int32_t* cu_seqlens,
+                                      pack3d_seq_index* idx, pack3d_stream_t stream);
+
+/* Synchronise the stream and report the index's error word: PACK3D_OK,
+ * PACK3D_ERR_LENGTHS, PACK3D_ERR_TIMEOUT or PACK3D_ERR_CUDA.  Blocks. */
+PACK3D_API int pack3d_seq_index_check(const pack3d_seq_index* idx, pack3d_stream_t stream);
+
+/* Forward: out and lse of every row of every sequence.  out must not overlap
+ * an input. */
+PACK3D_API int pack3d_seq_forward(const pack3d_seq_params* p, const pack3d_seq_index* idx,
+                                  const pack3d_seq_strides* strides, const void* q, const void* k,
+                                  const void* v, void* out, float* lse, pack3d_stream_t stream);
+
+/* Bytes of device workspace pack3d_seq_backward needs (8 bytes per query head
+ * and token); 0 if the params are invalid. */
+PACK3D_API size_t pack3d_seq_backward_workspace_bytes(const pack3d_seq_params* p);
+
+/* Backward: gradients of sum(dout * out) with respect to q, k and v (those of
+ * a shared key/value head summed over its query heads), from the forward's out
+ * and lse.  workspace: caller-allocated, 256-byte aligned; its contents on
+ * entry do not matter.  Calls that overlap on the GPU need one each.  The
+ * gradients must not overlap an input or each other. */
+PACK3D_API int pack3d_seq_backward(const pack3d_seq_params* p, const pack3d_seq_index* idx,
+                                   const pack3d_seq_strides* strides, const void* q, const void* k,
+                                   const void* v, const void* out, const float* lse,
+                                   const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                                   size_t workspace_bytes, pack3d_stream_t stream);
+
+/* Rotary positions.  The first rot_dim channels of each head turn in pairs,
+ * pair j by position * theta_j, theta_j = base^(-2j/rot_dim), and are multiplied
+ * by the amplitude; the others are copied.  Scalings for contexts longer than
+ * the original_length L the model was trained on:
+ *   LINEAR  theta_j / factor
+ *   BASE    base * factor^(rot_dim / (rot_dim - 2)): the slowest pair turns
+ *           factor times slower, the fastest as before
+ *   BANDS   by the turns n_j = L theta_j / 2 pi of a pair over L: theta_j where
+ *           n_j >= high, theta_j / factor where n_j <= low, their mix with weight
+ *           (n_j - low) / (high - low) between
+ *   RAMP    the mix by the pair's number: from theta_j at the pair that makes
+ *           high turns over L (rounded down) to theta_j / factor at the one that
+ *           makes low turns (rounded up); amplitude 0.1 ln(factor) + 1 */
+enum { PACK3D_ROTARY_HALF = 0, PACK3D_ROTARY_INTERLEAVED = 1 }; /* pairs (j, j + rot_dim/2) / (2j, 2j + 1) */
+enum {
+  PACK3D_ROTARY_NONE = 0,
+  PACK3D_ROTARY_LINEAR = 1,
+  PACK3D_ROTARY_BASE = 2,
+  PACK3D_ROTARY_BANDS = 3,
+  PACK3D_ROTARY_RAMP = 4
+};
+typedef struct {
+  int32_t n_tokens, Hq, Hk, head_dim; /* head_dim a multiple of 8, at most 256; Hk may be 0 */
+  int32_t rot_dim;                    /* even, 2 .. head_dim */
+  int32_t layout, dtype;
+  float base;                         /* > 0 (RAMP: > 1) */
+  int32_t scaling;
+  float factor;                       /* >= 1 (not read by NONE) */
+  int32_t original_length;            /* BANDS, RAMP */
+  float low, high;                    /* BANDS, RAMP: 0 < low < high, in turns */
+  float amplitude;                    /* 0: the scaling's own (1, RAMP 0.1 ln(factor) + 1) */
+  int64_t stride_q, stride_k, stride_q_out, stride_k_out; /* elements between rows; 0: no gaps */
+} pack3d_rotary_params;
+
+/* q_out = R(positions) q, k_out = R(positions) k (k, k_out ignored when Hk is
+ * 0), with any position >= 0 at full precision; rows whose position is
+ * negative are left as they were.  positions: int32 [n_tokens], device.
+ * q_out may be q and k_out may be k (same stride); no other overlap.  No
+ * workspace, no index: one token of each running sequence is the same call
+ * with n_tokens rows. */
+PACK3D_API int pack3d_rotary(const pack3d_rotary_params* p, const int32_t* positions,
+                             const void* q, const void* k, void* q_out, void* k_out,
+                             pack3d_stream_t stream);
+
+/* The gradient: dq = R(positions)^T dq_out, dk = R(positions)^T dk_out (the
+ * stride_* fields: of dq_out, dk_out, dq, dk in this order). */
+PACK3D_API int pack3d_rotary_backward(const pack3d_rotary_params* p, const int32_t* positions,
+                                      const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                      pack3d_stream_t stream);
 
 #ifdef __cplusplus
 }

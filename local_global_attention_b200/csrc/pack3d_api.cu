@@ -385,6 +385,8 @@ const char* pack3d_strerror(int status) {
     case PACK3D_ERR_CUDA: return "CUDA launch or runtime error";
     case PACK3D_ERR_TIMEOUT: return "bounded device-side wait timed out";
     case PACK3D_ERR_UNSUPPORTED: return "shape not built into this library";
+    case PACK3D_ERR_LENGTHS:
+      return "prefix sums of the lengths do not start at 0, fall, or end behind the tensors";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,53 @@
+// Internal declarations of the packed-sequence operators: dense attention over
+// sequences of different lengths packed one behind the other, and rotary
+// positions.
+#pragma once
+
+#include "pack3d_internal.cuh"
+
+namespace p3d {
+namespace seq {
+
+constexpr int ROWS = 128;  // rows of one attention tile (the M of one tcgen05 MMA)
+constexpr int PAIR = 256;  // query rows of one forward CTA: two tiles share each key/value load
+constexpr int MAX_DIM = 128;
+// Bits of the index's error word.
+constexpr int ERR_LENGTHS_BIT = 1, ERR_TIMEOUT_BIT = 4;
+
+// Shape derived once on the host from pack3d_seq_params and passed by value.
+struct SeqGeo {
+  int B, N;                // sequences, rows of the packed tensors
+  int Hq, Hk, G, d;        // G = Hq / Hk query heads share a key/value head
+  int causal;
+  float tau;               // softmax scale
+  int dtype;
+  int n_pair, n_rows;      // entries of the 256-row and of the 128-row tile lists
+};
+
+// Elements between two tokens of each tensor.
+struct Strides {
+  int64_t q, k, v, out, dout, dq, dk, dv;
+};
+
+// One tile of a sequence, as the lists hold it: the sequence's first row and
+// length, and the tile's first row in the sequence.  An unused entry has
+// length 0.
+struct Tile {
+  int start, len, off, pad;
+};
+
+int make_geo(const pack3d_seq_params* p, SeqGeo* g);
+int make_strides(const SeqGeo& g, const pack3d_seq_strides* s, Strides* out);
+
+int launch_build_index(const SeqGeo& g, const int32_t* cu, const pack3d_seq_index* ix,
+                       cudaStream_t s);
+int launch_forward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
+                        const void* q, const void* k, const void* v, void* out, float* lse,
+                        cudaStream_t s);
+int launch_backward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
+                         const void* q, const void* k, const void* v, const void* out,
+                         const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                         float* delta, cudaStream_t s);
+
+}  // namespace seq
+}  // namespace p3d

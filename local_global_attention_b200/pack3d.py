@@ -18,13 +18,19 @@ from . import build as _build
 BF16, FP32 = 0, 1
 ROPE_AXIAL, ROPE_PACKED = 0, 1  # axial RoPE on grid coordinates / 1-D RoPE on the packed index
 OK, ERR_ARG, ERR_COORDS, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
+ERR_LENGTHS = -6
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 EXPORTS = ("pack3d_index_bytes", "pack3d_index_init", "pack3d_build_index", "pack3d_index_check",
            "pack3d_block_summaries", "pack3d_forward_workspace_bytes", "pack3d_forward",
            "pack3d_window_forward", "pack3d_stage_kv", "pack3d_forward_staged",
            "pack3d_backward_workspace_bytes", "pack3d_backward", "pack3d_backward_summary_grads",
            "pack3d_backward_from_summary_grads", "pack3d_backward_noalloc",
-           "pack3d_kernel_launches", "pack3d_wait_selftest", "pack3d_strerror")
+           "pack3d_kernel_launches", "pack3d_wait_selftest", "pack3d_strerror",
+           "pack3d_seq_index_bytes", "pack3d_seq_index_init", "pack3d_seq_build_index",
+           "pack3d_seq_index_check", "pack3d_seq_forward", "pack3d_seq_backward_workspace_bytes",
+           "pack3d_seq_backward", "pack3d_rotary", "pack3d_rotary_backward")
 
 
 class Params(ctypes.Structure):
@@ -43,6 +49,30 @@ class Index(ctypes.Structure):
                 ("bcount", ctypes.c_void_p), ("bocc", ctypes.c_void_p),
                 ("tile", ctypes.c_int32 * 3), ("n_tiles", ctypes.c_int32),
                 ("n_halo", ctypes.c_int64)]
+
+
+class SeqParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_tokens", "Hq", "Hk", "head_dim",
+                                              "causal")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class SeqStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("q", "k", "v", "out", "dout", "dq", "dk", "dv")]
+
+
+class SeqIndexStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pos", "seq", "pair", "query", "key", "err")] + [
+        ("n_pair", ctypes.c_int32), ("n_rows", ctypes.c_int32)]
+
+
+class RotaryParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "Hq", "Hk", "head_dim", "rot_dim",
+                                              "layout", "dtype")] + [
+        ("base", ctypes.c_float), ("scaling", ctypes.c_int32), ("factor", ctypes.c_float),
+        ("original_length", ctypes.c_int32), ("low", ctypes.c_float), ("high", ctypes.c_float),
+        ("amplitude", ctypes.c_float)] + [
+        (n, ctypes.c_int64) for n in ("stride_q", "stride_k", "stride_q_out", "stride_k_out")]
 
 
 class Pack3dError(RuntimeError):
@@ -97,6 +127,18 @@ def load(build_if_missing: bool = True):
                                                            ctypes.c_size_t, vp, vp, vp, vp]
         lib.pack3d_backward_noalloc.argtypes = [P(Params), P(Index), vp, vp, vp, vp, vp, vp, vp,
                                                 vp, vp, vp]
+        sp, si, ss = P(SeqParams), P(SeqIndexStruct), P(SeqStrides)
+        lib.pack3d_seq_index_bytes.argtypes = [sp]
+        lib.pack3d_seq_index_bytes.restype = ctypes.c_size_t
+        lib.pack3d_seq_index_init.argtypes = [sp, vp, ctypes.c_size_t, si]
+        lib.pack3d_seq_build_index.argtypes = [sp, vp, si, vp]
+        lib.pack3d_seq_index_check.argtypes = [si, vp]
+        lib.pack3d_seq_forward.argtypes = [sp, si, ss, vp, vp, vp, vp, vp, vp]
+        lib.pack3d_seq_backward_workspace_bytes.argtypes = [sp]
+        lib.pack3d_seq_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.pack3d_seq_backward.argtypes = [sp, si, ss, *([vp] * 10), ctypes.c_size_t, vp]
+        lib.pack3d_rotary.argtypes = [P(RotaryParams), *([vp] * 6)]
+        lib.pack3d_rotary_backward.argtypes = [P(RotaryParams), *([vp] * 6)]
         lib.pack3d_wait_selftest.argtypes = [ctypes.c_uint32, vp]
         lib.pack3d_kernel_launches.argtypes = []
         lib.pack3d_kernel_launches.restype = ctypes.c_uint64
@@ -433,3 +475,291 @@ class Pack3D:
 
     def backward(self, q, k, v, out, lse, dout, stream=None):
         return pack3d_backward(self.params, self.index, q, k, v, out, lse, dout, stream=stream)
+
+
+# ---- packed sequences: dense attention and rotary positions ------------------------------
+
+_DTYPES = {"bf16": BF16, "fp32": FP32, torch.bfloat16: BF16, torch.float32: FP32}
+_TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
+
+
+def make_seq_params(n_seqs: int, n_tokens: int, heads: int, kv_heads: int = None,
+                    head_dim: int = 96, causal: bool = True, dtype="bf16",
+                    scale: float = 0.0) -> SeqParams:
+    """Params of attention over ``n_seqs`` sequences in packed tensors of
+    ``n_tokens`` rows; ``kv_heads`` (default: ``heads``) divides ``heads``,
+    ``scale`` 0 selects 1 / sqrt(head_dim)."""
+    return SeqParams(n_seqs, n_tokens, heads, heads if kv_heads is None else kv_heads, head_dim,
+                     int(bool(causal)), float(scale), _DTYPES[dtype])
+
+
+def make_rotary_params(head_dim: int, rot_dim: int = None, layout: str = "half",
+                       base: float = 10000.0, dtype="bf16", scaling: str = "none",
+                       factor: float = 1.0, original_length: int = 0, low: float = 0.0,
+                       high: float = 0.0, amplitude: float = 0.0) -> RotaryParams:
+    """Params of the rotary calls; ``rot_dim`` defaults to the whole head,
+    ``amplitude`` 0 selects the scaling's own.  The rows, heads and strides are
+    taken from the tensors of each call."""
+    return RotaryParams(head_dim=head_dim, rot_dim=head_dim if rot_dim is None else rot_dim,
+                        layout=ROTARY_LAYOUTS[layout], dtype=_DTYPES[dtype], base=float(base),
+                        scaling=ROTARY_SCALINGS[scaling], factor=float(factor),
+                        original_length=int(original_length), low=float(low), high=float(high),
+                        amplitude=float(amplitude))
+
+
+class _Launch:
+    """The device and stream of one packed-sequence call: every tensor on one
+    device, which is current while the call launches; the given stream (of that
+    device) or the device's current one.  Buffers allocated here are recorded on
+    a given stream, so that the allocator does not hand them on early."""
+
+    def __init__(self, like, stream):
+        if not like.is_cuda:
+            raise ValueError("PACK3D tensors must be CUDA tensors")
+        self.device, self.given = like.device, None
+        if stream is None:
+            self.raw = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            if stream.device != self.device:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+            self.given, self.raw = stream, stream.cuda_stream
+        self.before = None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.device.index:
+            self.before = now
+            torch.cuda.set_device(self.device)
+        return self
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+
+    def rows(self, t, shape, dtype, what):
+        """The token stride of a [rows, heads, head_dim] tensor whose heads and
+        channels lie without gaps."""
+        if t.device != self.device:
+            raise ValueError(f"{what} is on {t.device}, not on {self.device}")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} is {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        n, h, d = shape
+        s = t.stride()
+        if n * h * d and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+            raise ValueError(f"{what}: the heads and channels of a token must be contiguous")
+        if n <= 1:
+            return 0
+        if s[0] < h * d or s[0] % 8:
+            raise ValueError(f"{what}: the token stride {s[0]} must be a multiple of 8 and at "
+                             f"least {h * d}")
+        return s[0]
+
+    def flat(self, t, shape, dtype, what):
+        if t.device != self.device or t.dtype != dtype or t.shape != shape or \
+                not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on "
+                             f"{self.device}")
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.given is not None:
+            t.record_stream(self.given)
+        return t
+
+
+class SeqIndex:
+    """A built index of a pack: the device buffer and the C struct over it."""
+
+    def __init__(self, params: SeqParams, device=None):
+        lib = load()
+        nbytes = lib.pack3d_seq_index_bytes(ctypes.byref(params))
+        if nbytes == 0:
+            raise Pack3dError(ERR_ARG, "pack3d_seq_index_bytes")
+        self.params = params
+        self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self.struct = SeqIndexStruct()
+        base = self.buffer.data_ptr()
+        _check(lib.pack3d_seq_index_init(ctypes.byref(params), base + (-base) % 256, nbytes,
+                                         ctypes.byref(self.struct)), "pack3d_seq_index_init")
+
+    def _rows(self, field):
+        off = getattr(self.struct, field) - self.buffer.data_ptr()
+        return self.buffer[off:off + 4 * self.params.n_tokens].view(torch.int32)
+
+    @property
+    def positions(self):
+        """int32 [n_tokens]: each row's position in its sequence (-1 behind the last)."""
+        return self._rows("pos")
+
+    @property
+    def sequences(self):
+        """int32 [n_tokens]: the number of each row's sequence (-1 behind the last)."""
+        return self._rows("seq")
+
+
+def pack3d_seq_build_index(params: SeqParams, cu_seqlens: torch.Tensor, index: SeqIndex = None,
+                           stream=None) -> SeqIndex:
+    """Index of a pack from the prefix sums of its lengths (int32 [n_seqs + 1])."""
+    with _Launch(cu_seqlens, stream) as at:
+        at.flat(cu_seqlens, (params.n_seqs + 1,), torch.int32, "cu_seqlens")
+        if index is None:
+            index = SeqIndex(params, device=at.device)
+            if at.given is not None:
+                index.buffer.record_stream(at.given)
+        elif index.buffer.device != at.device:
+            raise ValueError(f"the index is on {index.buffer.device}, not on {at.device}")
+        _check(load().pack3d_seq_build_index(params, cu_seqlens.data_ptr(), index.struct, at.raw),
+               "pack3d_seq_build_index")
+    return index
+
+
+def pack3d_seq_index_check(index: SeqIndex, stream=None) -> int:
+    """Synchronise and return the index status code (0, ERR_LENGTHS, ERR_TIMEOUT)."""
+    with _Launch(index.buffer, stream) as at:
+        return int(load().pack3d_seq_index_check(index.struct, at.raw))
+
+
+def _seq_call(params, index, at):
+    if index.buffer.device != at.device:
+        raise ValueError(f"the index is on {index.buffer.device}, not on {at.device}")
+    n, d, dt = params.n_tokens, params.head_dim, _TORCH_DTYPE[params.dtype]
+    return (n, params.Hq, d), (n, params.Hk, d), (params.Hq, n), dt
+
+
+def pack3d_seq_forward(params: SeqParams, index: SeqIndex, q, k, v, out=None, lse=None,
+                       stream=None):
+    """Attention over every sequence of the pack: (out, lse).  q, k, v may be
+    slices of one tensor (any token stride that is a multiple of 8 elements).
+    Rows behind the last sequence are left as they were."""
+    with _Launch(q, stream) as at:
+        qs, ks, ls, dt = _seq_call(params, index, at)
+        st = SeqStrides(q=at.rows(q, qs, dt, "q"), k=at.rows(k, ks, dt, "k"),
+                        v=at.rows(v, ks, dt, "v"))
+        if out is None:
+            out = at.empty(qs, dt)
+        else:
+            st.out = at.rows(out, qs, dt, "out")
+        if lse is None:
+            lse = at.empty(ls, torch.float32)
+        else:
+            at.flat(lse, ls, torch.float32, "lse")
+        _check(load().pack3d_seq_forward(params, index.struct, st, q.data_ptr(), k.data_ptr(),
+                                         v.data_ptr(), out.data_ptr(), lse.data_ptr(), at.raw),
+               "pack3d_seq_forward")
+    return out, lse
+
+
+def pack3d_seq_backward_workspace_bytes(params: SeqParams) -> int:
+    return int(load().pack3d_seq_backward_workspace_bytes(ctypes.byref(params)))
+
+
+def pack3d_seq_backward(params: SeqParams, index: SeqIndex, q, k, v, out, lse, dout, dq=None,
+                        dk=None, dv=None, workspace=None, stream=None):
+    """Gradients (dq, dk, dv) from the forward's out and lse."""
+    with _Launch(q, stream) as at:
+        qs, ks, ls, dt = _seq_call(params, index, at)
+        st = SeqStrides(q=at.rows(q, qs, dt, "q"), k=at.rows(k, ks, dt, "k"),
+                        v=at.rows(v, ks, dt, "v"), out=at.rows(out, qs, dt, "out"),
+                        dout=at.rows(dout, qs, dt, "dout"))
+        at.flat(lse, ls, torch.float32, "lse")
+        if dq is None:
+            dq = at.empty(qs, dt)
+        else:
+            st.dq = at.rows(dq, qs, dt, "dq")
+        if dk is None:
+            dk = at.empty(ks, dt)
+        else:
+            st.dk = at.rows(dk, ks, dt, "dk")
+        if dv is None:
+            dv = at.empty(ks, dt)
+        else:
+            st.dv = at.rows(dv, ks, dt, "dv")
+        if workspace is None:
+            workspace = at.empty((pack3d_seq_backward_workspace_bytes(params),), torch.uint8)
+        elif workspace.device != at.device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on {at.device}")
+        _check(load().pack3d_seq_backward(params, index.struct, st, q.data_ptr(), k.data_ptr(),
+                                          v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                          dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                          dv.data_ptr(), workspace.data_ptr(),
+                                          workspace.numel() * workspace.element_size(), at.raw),
+               "pack3d_seq_backward")
+    return dq, dk, dv
+
+
+def _rotary(name, params, positions, q, k, q_out, k_out, stream):
+    with _Launch(q, stream) as at:
+        dt, d = _TORCH_DTYPE[params.dtype], params.head_dim
+        if q.dim() != 3 or (k is not None and k.dim() != 3):
+            raise ValueError("q and k must be [rows, heads, head_dim]")
+        n, qs = q.shape[0], (q.shape[0], q.shape[1], d)
+        at.flat(positions, (n,), torch.int32, "positions")
+        p = RotaryParams.from_buffer_copy(params)
+        p.n_tokens, p.Hq, p.Hk = n, q.shape[1], 0
+        p.stride_q = at.rows(q, qs, dt, "q")
+        if q_out is None:
+            q_out = at.empty(qs, dt)
+        else:
+            p.stride_q_out = at.rows(q_out, qs, dt, "q_out")
+        if k is not None:
+            ks = (n, k.shape[1], d)
+            p.Hk, p.stride_k = k.shape[1], at.rows(k, ks, dt, "k")
+            if k_out is None:
+                k_out = at.empty(ks, dt)
+            else:
+                p.stride_k_out = at.rows(k_out, ks, dt, "k_out")
+        _check(getattr(load(), name)(p, positions.data_ptr(), q.data_ptr(),
+                                     None if k is None else k.data_ptr(), q_out.data_ptr(),
+                                     None if k is None else k_out.data_ptr(), at.raw), name)
+    return q_out if k is None else (q_out, k_out)
+
+
+def pack3d_rotary(params: RotaryParams, positions, q, k=None, q_out=None, k_out=None,
+                  stream=None):
+    """Turn q [rows, heads, head_dim] and k by their rows' positions (int32);
+    returns q_out, or (q_out, k_out) with k.  ``q_out=q, k_out=k`` turns them in
+    place.  Rows with a negative position are left as they were."""
+    return _rotary("pack3d_rotary", params, positions, q, k, q_out, k_out, stream)
+
+
+def pack3d_rotary_backward(params: RotaryParams, positions, dq_out, dk_out=None, dq=None, dk=None,
+                           stream=None):
+    """Gradients of pack3d_rotary's inputs from those of its outputs."""
+    return _rotary("pack3d_rotary_backward", params, positions, dq_out, dk_out, dq, dk, stream)
+
+
+class SeqAttention:
+    """Convenience wrapper: one pack shape, its index, and the calls; ``rotary``
+    (RotaryParams) turns q and k by their positions in their sequences first."""
+
+    def __init__(self, params: SeqParams, rotary: RotaryParams = None):
+        self.params, self.rotary, self.index = params, rotary, None
+
+    def build_index(self, cu_seqlens, stream=None, check=True):
+        self.index = pack3d_seq_build_index(self.params, cu_seqlens, self.index, stream)
+        if check:
+            _check(pack3d_seq_index_check(self.index, stream), "pack3d_seq_index_check")
+        return self.index
+
+    def rotate(self, q, k, stream=None):
+        """q and k at their positions (as they are without ``rotary``)."""
+        if self.rotary is None:
+            return q, k
+        return pack3d_rotary(self.rotary, self.index.positions, q, k, stream=stream)
+
+    def forward(self, q, k, v, stream=None):
+        """(out, lse, (q, k) at their positions, which the backward takes)."""
+        qr, kr = self.rotate(q, k, stream)
+        return (*pack3d_seq_forward(self.params, self.index, qr, kr, v, stream=stream), (qr, kr))
+
+    def backward(self, rotated, v, out, lse, dout, stream=None):
+        qr, kr = rotated
+        dq, dk, dv = pack3d_seq_backward(self.params, self.index, qr, kr, v, out, lse, dout,
+                                         stream=stream)
+        if self.rotary is not None:
+            pack3d_rotary_backward(self.rotary, self.index.positions, dq, dk, dq, dk, stream)
+        return dq, dk, dv
