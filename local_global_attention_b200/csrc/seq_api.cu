@@ -162,6 +162,8 @@ int pack3d_seq_forward(const pack3d_seq_params* p, const pack3d_seq_index* idx,
   if (g.N == 0) return PACK3D_OK;  // every sequence is empty
   if (!q || !k || !v || !out || !lse || !aligned(q, k, v, out) || ((uintptr_t)lse & 3))
     return PACK3D_ERR_ARG;
+  if (g.dtype == PACK3D_BF16)
+    return launch_forward_tc(g, st, idx, q, k, v, out, lse, (cudaStream_t)stream);
   return launch_forward_simt(g, st, idx, q, k, v, out, lse, (cudaStream_t)stream);
 }
 

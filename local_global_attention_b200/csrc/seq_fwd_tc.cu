@@ -1,0 +1,379 @@
+// Packed-sequence attention, forward, on the Blackwell tensor cores (bf16 in,
+// fp32 accumulate).
+//
+//   S_ij = tau q_i . k_j over the row's own sequence (j <= i when causal),
+//   out_i = sum_j exp(S_ij - lse_i) v_j,  lse_i = ln sum_j exp S_ij,
+// in one pass over the keys with a running maximum m and sum l: per key tile
+//   P = 2^(c S - m),  l += row sum of P,  O += P v,   c = tau log2 e,
+// and out = O / l.  m moves only when a row's maximum grows by more than 8
+// (log2 units), so O, in tensor memory, is rarely rescaled; P then stays below
+// 2^8, which bf16 holds as precisely as values below 1.  l sums the unrounded P
+// in fp32; P is rounded to bf16 as the operand of the product with v.
+//
+// One CTA per (256 query rows of a sequence, head): two tiles of 128 rows that
+// share every key/value tile loaded, which halves the L2 reads per product (a
+// 128-row CTA would need 64 bytes per clock and SM at head_dim 128, about twice
+// what L2 gives).  Roles:
+//   * warps 0-3 and 4-7: the softmax of tile 0 and of tile 1, a row per thread;
+//   * warp 8: the MMAs (one elected lane), ordered
+//       S0(0) S1(0) | PV0(j) S0(j+1) PV1(j) S1(j+1) | ...
+//     so one tile's products run while the other tile's softmax works;
+//   * warp 9: TMA loads of q, k and v, and zeros over the v rows behind the
+//     sequence's end in its last tile.
+// Tensor memory: S0, S1 (128 columns of fp32 each; P as bf16 over the first 64),
+// O0, O1.  The products of one tile are issued in order, so S(j+1) over P(j)
+// needs no wait for PV(j), and a softmax warp that sees S(j) complete knows that
+// PV(j-1) is too, when it rescales O.
+//
+// Masked logits are set to -inf by a select in the tiles that need it: the
+// diagonal one, and the last one of a sequence whose length is no multiple of
+// 128.  Every wait is bounded; a CTA that gives up sets the timeout bit of the
+// index's error word.
+#include <cuda.h>
+#include <math.h>
+
+#include "seq_tc.cuh"
+
+namespace p3d {
+namespace seq {
+
+namespace {
+
+constexpr int MMA_WARP = 8, TMA_WARP = 9, NT = 320;
+constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;
+constexpr float RESCALE_THRESHOLD = 8.0f;
+
+template <int HD>
+struct Cfg {
+  static constexpr int NSEG = HD > 64 ? 2 : 1;
+  static constexpr uint32_t TILE = NSEG * SEG;
+  // key and value tiles in flight: what 227 KB hold beside the two query tiles
+  static constexpr int NST = HD > 64 ? 5 : 8;
+};
+
+template <int HD>
+struct Smem {
+  uint8_t q[2][Cfg<HD>::TILE];
+  uint8_t kv[Cfg<HD>::NST][Cfg<HD>::TILE];  // ring: k_0, v_0, k_1, v_1, ...
+  uint64_t q_full[2];
+  uint64_t full[Cfg<HD>::NST], empty[Cfg<HD>::NST];
+  uint64_t s_full[2];     // S of the tile's next key tile computed
+  uint64_t p_full[2][2];  // the first and second 64 columns of P written
+  uint64_t o_done[2];     // every product of the tile done
+  uint64_t v_fixed;       // rows behind the sequence's end are zero
+  uint64_t drain;
+  uint32_t tmem_base;
+  int32_t abort;
+};
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
+// P = 2^(S c - m) of 32 keys into 16 words; returns the sum.
+__device__ __forceinline__ float exp_pack(const uint32_t* sv, float c2, float mneg, uint32_t* p) {
+  float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 cc = make_float2(c2, c2), mm = make_float2(mneg, mneg);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 a = f2_fma(make_float2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])),
+                            cc, mm);
+    const float2 e = make_float2(ex2(a.x), ex2(a.y));
+    acc[i & 1] = f2_add(acc[i & 1], e);
+    p[i] = pack_bf16x2(e.x, e.y);
+  }
+  const float2 t = f2_add(acc[0], acc[1]);
+  return t.x + t.y;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(NT, 1)
+    k_seq_forward_tc(SeqGeo g, int64_t stride_out, pack3d_seq_index ix,
+                     const __grid_constant__ Maps maps, __nv_bfloat16* __restrict__ out,
+                     float* __restrict__ lse) {
+  using C = Cfg<HD>;
+  constexpr int NSEG = C::NSEG, NST = C::NST;
+  if (ix.err[0]) return;
+  const int h = blockIdx.x % g.Hq;
+  const Tile t = reinterpret_cast<const Tile*>(ix.pair)[blockIdx.x / g.Hq];
+  if (t.len == 0) return;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<HD>& sm = *reinterpret_cast<Smem<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~(uintptr_t)1023);
+  volatile int32_t* abort_flag = &sm.abort;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  // key tiles that each query tile visits (the second one may have no rows)
+  auto tiles_of = [&](int i) {
+    const int first = t.off + i * ROWS;
+    if (first >= t.len) return 0;
+    return ((g.causal ? min(t.len, first + ROWS) : t.len) + ROWS - 1) / ROWS;
+  };
+  const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
+  const bool fix = n * ROWS > t.len;  // the last key tile ends behind the sequence
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i][0], 4);  // one arrival per softmax warp
+      mbar_init(&sm.p_full[i][1], 4);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    mbar_init(&sm.v_fixed, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(&sm.tmem_base, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = sm.tmem_base;
+
+  if (warp == TMA_WARP) {
+    // ================= TMA producer (lane 0) =================
+    const int hk = h / g.G, row0 = t.start + t.off;
+    int issued = 0;
+    if (lane == 0) {
+      bool ok = true;
+      mbar_arrive_expect_tx(&sm.q_full[0], C::TILE);
+      load_tile_tma<NSEG>(sm.q[0], &maps.q, h, row0, &sm.q_full[0]);
+      for (int i = 0; i < 2 * n && ok; ++i) {
+        const int s = i % NST, round = i / NST;
+        if (round > 0 &&
+            !(ok = mbar_wait_or_abort(&sm.empty[s], (round - 1) & 1, WAIT_LIMIT, abort_flag)))
+          break;
+        mbar_arrive_expect_tx(&sm.full[s], C::TILE);
+        load_tile_tma<NSEG>(sm.kv[s], (i & 1) ? &maps.v : &maps.k, hk, t.start + (i / 2) * ROWS,
+                            &sm.full[s]);
+        if (i == 0 && n1 > 0) {
+          mbar_arrive_expect_tx(&sm.q_full[1], C::TILE);
+          load_tile_tma<NSEG>(sm.q[1], &maps.q, h, row0 + ROWS, &sm.q_full[1]);
+        }
+        issued = i + 1;
+      }
+    }
+    issued = __shfl_sync(0xffffffffu, issued, 0);
+    if (fix && issued == 2 * n) {
+      const int i = 2 * n - 1, s = i % NST;
+      if (warp_wait(&sm.full[s], (i / NST) & 1, abort_flag)) {
+        zero_rows<NSEG>(sm.kv[s], t.len - (n - 1) * ROWS, lane);
+        if (lane == 0) mbar_arrive(&sm.v_fixed);
+      }
+    }
+    // Copies still in flight must land before the CTA ends (bounded).
+    if (lane == 0) {
+      mbar_wait(&sm.q_full[0], 0, WAIT_LIMIT);
+      if (n1 > 0 && issued > 0) mbar_wait(&sm.q_full[1], 0, WAIT_LIMIT);
+      for (int i = max(0, issued - NST); i < issued; ++i)
+        mbar_wait(&sm.full[i % NST], (i / NST) & 1, WAIT_LIMIT);
+    }
+    __syncwarp();
+  } else if (warp == MMA_WARP) {
+    // ================= MMA issue (the whole warp, converged; one lane issues) =================
+    constexpr uint32_t idesc_s = idesc_bf16(ROWS, ROWS, false);
+    constexpr uint32_t idesc_o = idesc_bf16(ROWS, HD, true);
+    const uint64_t qd = sdesc_sw128(smem_u32(sm.q[0])), kvd = sdesc_sw128(smem_u32(sm.kv[0]));
+    auto wait_item = [&](int i) {
+      return warp_wait(&sm.full[i % NST], (i / NST) & 1, abort_flag);
+    };
+    auto issue_s = [&](int i, int j) {
+      const uint32_t dS = tbase + COL_S + ROWS * i;
+      const uint64_t a = qd + (uint64_t)((i * C::TILE) >> 4);
+      const uint64_t b = kvd + (uint64_t)((((2 * j) % NST) * C::TILE) >> 4);
+#pragma unroll
+      for (int st = 0; st < HD / 16; ++st)
+        mma_ss_warp(dS, a + k_step(st), b + k_step(st), idesc_s, st > 0);
+      mma_commit_warp(&sm.s_full[i]);
+    };
+    auto issue_pv = [&](int i, int j, int half) {
+      const uint32_t pS = tbase + COL_S + ROWS * i;
+      const uint64_t b = kvd + (uint64_t)((((2 * j + 1) % NST) * C::TILE) >> 4);
+#pragma unroll
+      for (int st = 4 * half; st < 4 * half + 4; ++st)
+        mma_ts_warp(tbase + COL_O + HD * i, pS + 8 * st, b + row_step(st), idesc_o,
+                    (j > 0 || st > 0) ? 1u : 0u);
+    };
+    bool ok = warp_wait(&sm.q_full[0], 0, abort_flag) && wait_item(0);
+    if (ok) {
+      tc_fence_after();
+      issue_s(0, 0);
+      if (n1 > 0 && (ok = warp_wait(&sm.q_full[1], 0, abort_flag))) {
+        tc_fence_after();
+        issue_s(1, 0);
+      }
+      mma_commit_warp(&sm.empty[0]);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      if (!(ok = wait_item(2 * j + 1))) break;
+      if (fix && j == n - 1 && !(ok = warp_wait(&sm.v_fixed, 0, abort_flag))) break;
+      if (j + 1 < n && !(ok = wait_item(2 * j + 2))) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ni = i ? n1 : n0;
+        if (j >= ni || !ok) continue;
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = warp_wait(&sm.p_full[i][half], j & 1, abort_flag))) break;
+          tc_fence_after();
+          issue_pv(i, j, half);
+        }
+        if (!ok) break;
+        if (j + 1 < ni)
+          issue_s(i, j + 1);
+        else
+          mma_commit_warp(&sm.o_done[i]);
+      }
+      mma_commit_warp(&sm.empty[(2 * j + 1) % NST]);
+      if (j + 1 < n) mma_commit_warp(&sm.empty[(2 * j + 2) % NST]);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax (one query row per thread) =================
+    const int i = warp >> 2, ni = i ? n1 : n0;
+    const int r = tid & (ROWS - 1);
+    const int pos = t.off + i * ROWS + r;  // position in the sequence
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tbase + lane_base + COL_S + ROWS * i;
+    const uint32_t tO = tbase + lane_base + COL_O + HD * i;
+    const float c2 = g.tau * LOG2E;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    for (int j = 0; j < ni; ++j) {
+      if (!(ok = warp_wait(&sm.s_full[i], j & 1, abort_flag))) break;
+      tc_fence_after();
+      uint32_t sv[ROWS];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+      tmem_wait_ld();
+      if (j == ni - 1 && (g.causal || fix)) {
+        // the diagonal tile, or the end of the sequence
+        const int last = min(g.causal ? pos : t.len - 1, t.len - 1) - j * ROWS;
+#pragma unroll
+        for (int c = 0; c < ROWS; ++c)
+          if (c > last) sv[c] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(sv[c]);
+#pragma unroll
+      for (int c = 4; c < ROWS; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(sv[c]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+      float corr = 1.f;
+      if (top > m_run + RESCALE_THRESHOLD) {
+        corr = ex2(m_run - top);
+        l_run *= corr;
+        m_run = top;
+      }
+      if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+#pragma unroll
+        for (int c = 0; c < HD / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+          tmem_st32(tO + 32 * c, o);
+        }
+      }
+      // a row of -inf logits only (none of finite inputs has one) stays at weight 0
+      const float mneg = m_run == -INFINITY ? 0.f : -m_run;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+        l_run += exp_pack(sv + 64 * half, c2, mneg, p);
+        l_run += exp_pack(sv + 64 * half + 32, c2, mneg, p + 16);
+        tmem_st32(tS + 32 * half, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[i][half]);
+      }
+    }
+    if (ok && ni > 0) ok = warp_wait(&sm.o_done[i], 0, abort_flag);
+    if (ok && ni > 0) {
+      tc_fence_after();
+      const float inv = 1.f / l_run;
+      const int64_t row = (int64_t)t.start + pos;
+      __nv_bfloat16* dst = out + row * stride_out + (int64_t)h * g.d;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * c, o);
+        tmem_wait_ld();
+        if (pos < t.len) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int ch = 32 * c + 8 * e;
+            if (ch >= g.d) break;
+            const float2 f = make_float2(inv, inv);
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 y = f2_mul(make_float2(__uint_as_float(o[8 * e + 2 * x]),
+                                                  __uint_as_float(o[8 * e + 2 * x + 1])),
+                                      f);
+              w[x] = pack_bf16x2(y.x, y.y);
+            }
+            *reinterpret_cast<uint4*>(dst + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (pos < t.len) lse[(int64_t)h * g.N + row] = (m_run + log2f(l_run)) * LN2;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (sm.abort && tid == 0) atomicOr(&ix.err[0], ERR_TIMEOUT_BIT);
+  if (warp == MMA_WARP) {
+    // A CTA that gave up may still have products in flight: they land before
+    // the columns are freed (bounded).
+    if (sm.abort) {
+      mma_commit_warp(&sm.drain);
+      if (lane == 0) mbar_wait(&sm.drain, 0, WAIT_LIMIT);
+      __syncwarp();
+    }
+    tc_fence_after();
+    tmem_dealloc(tbase, TMEM_COLS);
+  }
+}
+
+template <int HD>
+int forward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, const void* q,
+            const void* k, const void* v, void* out, float* lse, cudaStream_t s) {
+  Maps maps;
+  if (!encode_rows(&maps.q, q, g.d, g.Hq, g.N, st.q, ROWS) ||
+      !encode_rows(&maps.k, k, g.d, g.Hk, g.N, st.k, ROWS) ||
+      !encode_rows(&maps.v, v, g.d, g.Hk, g.N, st.v, ROWS))
+    return PACK3D_ERR_CUDA;
+  constexpr size_t bytes = sizeof(Smem<HD>) + 1024;  // + alignment slack
+  static_assert(bytes <= 232448, "shared memory of a CTA");
+  if (cudaFuncSetAttribute(k_seq_forward_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)bytes) != cudaSuccess)
+    return PACK3D_ERR_CUDA;
+  k_seq_forward_tc<HD><<<(unsigned)(g.n_pair * g.Hq), NT, bytes, s>>>(
+      g, st.out, *ix, maps, (__nv_bfloat16*)out, lse);
+  count_launches(1);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+int launch_forward_tc(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
+                      const void* q, const void* k, const void* v, void* out, float* lse,
+                      cudaStream_t s) {
+  if (g.d <= 64) return forward<64>(g, st, ix, q, k, v, out, lse, s);
+  if (g.d <= 96) return forward<96>(g, st, ix, q, k, v, out, lse, s);
+  return forward<128>(g, st, ix, q, k, v, out, lse, s);
+}
+
+}  // namespace seq
+}  // namespace p3d

@@ -44,6 +44,9 @@ int launch_build_index(const SeqGeo& g, const int32_t* cu, const pack3d_seq_inde
 int launch_forward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
                         const void* q, const void* k, const void* v, void* out, float* lse,
                         cudaStream_t s);
+int launch_forward_tc(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
+                      const void* q, const void* k, const void* v, void* out, float* lse,
+                      cudaStream_t s);
 int launch_backward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
                          const void* q, const void* k, const void* v, const void* out,
                          const float* lse, const void* dout, void* dq, void* dk, void* dv,

@@ -389,16 +389,9 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
 int launch_forward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
                         const void* q, const void* k, const void* v, void* out, float* lse,
                         cudaStream_t s) {
-  using B = __nv_bfloat16;
-  const bool b = g.dtype == PACK3D_BF16;
-  if (g.d <= 64)
-    return b ? forward<B, 64>(g, st, ix, q, k, v, out, lse, s)
-             : forward<float, 64>(g, st, ix, q, k, v, out, lse, s);
-  if (g.d <= 96)
-    return b ? forward<B, 96>(g, st, ix, q, k, v, out, lse, s)
-             : forward<float, 96>(g, st, ix, q, k, v, out, lse, s);
-  return b ? forward<B, 128>(g, st, ix, q, k, v, out, lse, s)
-           : forward<float, 128>(g, st, ix, q, k, v, out, lse, s);
+  if (g.d <= 64) return forward<float, 64>(g, st, ix, q, k, v, out, lse, s);
+  if (g.d <= 96) return forward<float, 96>(g, st, ix, q, k, v, out, lse, s);
+  return forward<float, 128>(g, st, ix, q, k, v, out, lse, s);
 }
 
 int launch_backward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,

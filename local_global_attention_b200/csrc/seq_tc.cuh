@@ -1,0 +1,90 @@
+// Pieces shared by the tensor-core kernels of packed-sequence attention: the
+// 128-byte-swizzled operand tiles, their descriptors and tensor maps, and the
+// converged-warp forms of waits.
+//
+// An operand tile is ROWS rows of one head, in segments of 64 channels: segment
+// s is [ROWS][128 bytes] with the 128-byte swizzle, the form in which a TMA box
+// of {64 channels, 1 head, ROWS rows} lands and which the MMAs read K-major
+// (channels contracted) or MN-major (rows contracted).  Channels from head_dim
+// on and rows behind the tensor are filled with zeros by the copy.
+#pragma once
+
+#include "seq_internal.cuh"
+#include "tc_attn_common.cuh"
+
+namespace p3d {
+namespace seq {
+
+using namespace tc;
+
+constexpr uint32_t SEG = ROWS * 128;  // bytes of one 64-channel segment of a tile
+constexpr uint32_t WAIT_LIMIT = 1u << 20;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// Matrix descriptor with the 128-byte swizzle (layout type 2): 8 rows of 128
+// bytes per swizzle atom, so the stride byte offset is 1024; the leading byte
+// offset is the distance of two 64-channel segments for an MN-major operand
+// (not read for a K-major one).
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(SEG >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Descriptor offset (16-byte units) of channel step st (16 channels) of a
+// K-major tile, and of row step st (16 rows) of an MN-major one.
+__host__ __device__ constexpr uint32_t k_step(int st) {
+  return ((st >> 2) * SEG + (st & 3) * 32) >> 4;
+}
+__host__ __device__ constexpr uint32_t row_step(int st) { return (uint32_t)(st * 16 * 128) >> 4; }
+
+// A wait of a whole converged warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
+                                          volatile int32_t* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, WAIT_LIMIT, abort));
+}
+
+// Rows [from, ROWS) of a tile set to zero by one warp, visible to the tensor
+// core once the warp has arrived on a barrier: what stands behind the last row
+// of a sequence (the next sequence, or anything) must not enter a product that
+// contracts rows, where even a weight of zero passes a NaN on.
+template <int NSEG>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
+  for (int i = from * 8 + lane; i < ROWS * 8; i += 32)
+#pragma unroll
+    for (int s = 0; s < NSEG; ++s)
+      *reinterpret_cast<uint4*>(tile + s * SEG + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Tensor map of a packed tensor [N][H][d] (tokens `stride` elements apart):
+// boxes of {64 channels, 1 head, `rows` rows}.
+inline bool encode_rows(CUtensorMap* m, const void* base, int d, int H, int N, int64_t stride,
+                        int rows) {
+  tca::EncodeTiled fn = tca::encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)N};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, step[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// One tile (all segments) of a head by TMA; returns nothing, signals `bar`.
+template <int NSEG>
+__device__ __forceinline__ void load_tile_tma(uint8_t* dst, const CUtensorMap* map, int head,
+                                              int row, uint64_t* bar) {
+#pragma unroll
+  for (int s = 0; s < NSEG; ++s) tma_load_3d(dst + s * SEG, map, 64 * s, head, row, bar);
+}
+
+}  // namespace seq
+}  // namespace p3d
