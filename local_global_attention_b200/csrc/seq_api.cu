@@ -188,8 +188,13 @@ int pack3d_seq_backward(const pack3d_seq_params* p, const pack3d_seq_index* idx,
     return PACK3D_ERR_ARG;
   if (!aligned(q, k, v, out, dout, dq, dk, dv) || ((uintptr_t)lse & 3)) return PACK3D_ERR_ARG;
   if (((uintptr_t)workspace & 255) || workspace_bytes < backward_bytes(g)) return PACK3D_ERR_ARG;
-  return launch_backward_simt(g, st, idx, q, k, v, out, lse, dout, dq, dk, dv, (float*)workspace,
-                              (cudaStream_t)stream);
+  float* delta = (float*)workspace;
+  if (g.dtype == PACK3D_FP32)
+    return launch_backward_simt(g, st, idx, q, k, v, out, lse, dout, dq, dk, dv, delta,
+                                (cudaStream_t)stream);
+  float* lse2 = (float*)((char*)workspace + backward_bytes(g) / 2);
+  return launch_backward_tc(g, st, idx, q, k, v, out, lse, dout, dq, dk, dv, delta, lse2,
+                            (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -51,6 +51,10 @@ int launch_backward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_in
                          const void* q, const void* k, const void* v, const void* out,
                          const float* lse, const void* dout, void* dq, void* dk, void* dv,
                          float* delta, cudaStream_t s);
+int launch_backward_tc(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix,
+                       const void* q, const void* k, const void* v, const void* out,
+                       const float* lse, const void* dout, void* dq, void* dk, void* dv,
+                       float* delta, float* lse2, cudaStream_t s);
 
 }  // namespace seq
 }  // namespace p3d

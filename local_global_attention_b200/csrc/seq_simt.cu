@@ -398,12 +398,10 @@ int launch_backward_simt(const SeqGeo& g, const Strides& st, const pack3d_seq_in
                          const void* q, const void* k, const void* v, const void* out,
                          const float* lse, const void* dout, void* dq, void* dk, void* dv,
                          float* delta, cudaStream_t s) {
-  using B = __nv_bfloat16;
-  const bool b = g.dtype == PACK3D_BF16;
 #define P3D_ARGS g, st, ix, q, k, v, out, lse, dout, dq, dk, dv, delta, s
-  if (g.d <= 64) return b ? backward<B, 64>(P3D_ARGS) : backward<float, 64>(P3D_ARGS);
-  if (g.d <= 96) return b ? backward<B, 96>(P3D_ARGS) : backward<float, 96>(P3D_ARGS);
-  return b ? backward<B, 128>(P3D_ARGS) : backward<float, 128>(P3D_ARGS);
+  if (g.d <= 64) return backward<float, 64>(P3D_ARGS);
+  if (g.d <= 96) return backward<float, 96>(P3D_ARGS);
+  return backward<float, 128>(P3D_ARGS);
 #undef P3D_ARGS
 }
 
