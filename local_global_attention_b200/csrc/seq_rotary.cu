@@ -12,13 +12,17 @@
 // position, then 2^-32 of a turn where its upper half becomes a float for
 // sincospi).  An fp32 product position * theta would be off by 0.03 rad there.
 //
-// Memory bound: every element is read and written once, 8 bytes or so of index
-// per row.  A thread owns one group of VEC pairs of a token and walks over
-// HEADS heads with the same cosines and sines in registers, so their ~40
-// instructions a pair are shared; consecutive threads cover a head's channels,
-// then the next heads of the same token, so a warp's accesses are whole rows.
-// VEC is the widest power of two (16 bytes at most) that divides the pair
-// segments, so odd rotated widths run with narrower accesses.
+// Memory bound: every element is read and written once, 4 bytes of index per
+// row.  A thread keeps one place of a row (a head's VEC pairs, or VEC channels
+// that are only copied) and walks over rows; per group of rows a block first
+// issues its loads, then computes the rows' cosines and sines once, one pair per
+// thread, into shared memory, where all heads of a row find them, then turns and
+// stores.  Consecutive threads cover a head, then the next heads, so a warp's
+// accesses are whole rows.  VEC is the widest power of two (16 bytes at most)
+// that divides the pair segments, so odd rotated widths run with narrower
+// accesses.  Measured at 65,536 rows x 16 heads x 96 (402 MB): 75 us, 5.4 TB/s,
+// 0.82 of the copy bandwidth; with cosines per thread, shared by four heads
+// only, and loads after them 126 us.
 #include <math.h>
 
 #include <algorithm>
@@ -31,17 +35,18 @@ namespace seq {
 namespace {
 
 constexpr int NT = 256;
-constexpr int MAX_PAIRS = 128;  // head_dim <= 256
+constexpr int MAX_PAIRS = 128;   // head_dim <= 256
+constexpr int MAX_HEADS = 65536; // of q and k together
+constexpr int CS_ENTRIES = 2048; // (cos, sin) pairs of a group of rows in shared memory
 
 struct RotArgs {
   uint64_t freq[MAX_PAIRS];  // theta_j / (2 pi), 64-bit binary fraction
   float amp, sense;          // sense -1: the transpose
   int half, r, d, n;         // pairs, rotated channels, head dim, rows
   int Hq, Hk;
-  int units;                 // threads of one (row, head group): pair groups, then copied groups
+  int units;                 // threads of a head: VEC pairs or channels turned, then copied
   int pair_units;
-  int splits;                // head groups of a row
-  int rows;                  // rows of a block
+  int cols, slots;           // threads of a row; rows side by side in a block
   int64_t sq, sk, soq, sok;  // elements between rows
 };
 
@@ -50,81 +55,107 @@ struct alignas(sizeof(T) * VEC) Vec {
   T x[VEC];
 };
 
-// HEADS: heads per thread.
-template <typename T, int VEC, int LAYOUT, int HEADS>
+// VEC values moved by one access of their whole width.
+template <int BYTES>
+struct Word;
+template <>
+struct Word<16> {
+  using type = uint4;
+};
+template <>
+struct Word<8> {
+  using type = uint2;
+};
+template <>
+struct Word<4> {
+  using type = uint32_t;
+};
+template <>
+struct Word<2> {
+  using type = uint16_t;
+};
+template <typename T, int VEC>
+__device__ __forceinline__ void load(Vec<T, VEC>& v, const T* src) {
+  using W = typename Word<sizeof(T) * VEC>::type;
+  *reinterpret_cast<W*>(&v) = *reinterpret_cast<const W*>(src);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store(T* dst, const Vec<T, VEC>& v) {
+  using W = typename Word<sizeof(T) * VEC>::type;
+  *reinterpret_cast<W*>(dst) = *reinterpret_cast<const W*>(&v);
+}
+
+// ROWS_T: rows of a thread per group.
+template <typename T, int VEC, int LAYOUT, int ROWS_T>
 __global__ void __launch_bounds__(NT)
     k_rotary(const __grid_constant__ RotArgs a, const int32_t* __restrict__ pos, const T* q,
              const T* k, T* qo, T* ko) {
-  const int cols = a.units * a.splits;
-  const int col = blockIdx.y * NT + threadIdx.x;
-  // cols <= NT: rows of a block side by side; else a block covers NT columns of one row
-  const int row_in = cols <= NT ? threadIdx.x / cols : 0;
-  const int c = cols <= NT ? threadIdx.x % cols : col;
-  const int64_t row = (int64_t)blockIdx.x * a.rows + row_in;
-  if (row_in >= a.rows || c >= cols || row >= a.n) return;
-  const int p = pos[row];
-  if (p < 0) return;  // a row behind the last sequence: left as it was
-  const int u = c % a.units, h0 = c / a.units;
+  constexpr bool HALF = LAYOUT == PACK3D_ROTARY_HALF;
+  constexpr int NP = HALF ? VEC : VEC / 2;  // pairs of a thread
   using V = Vec<T, VEC>;
-  const int H = a.Hq + a.Hk;
-  auto src = [&](int h) {
-    return h < a.Hq ? q + row * a.sq + (int64_t)h * a.d : k + row * a.sk + (int64_t)(h - a.Hq) * a.d;
-  };
-  auto dst = [&](int h) {
-    return h < a.Hq ? qo + row * a.soq + (int64_t)h * a.d
-                    : ko + row * a.sok + (int64_t)(h - a.Hq) * a.d;
-  };
-  if (u >= a.pair_units) {  // channels that are not rotated
-    const int ch = a.r + (u - a.pair_units) * VEC;
+  extern __shared__ float2 cs_all[];  // two of [rows of a group][pairs]
+  __shared__ uint64_t freq[MAX_PAIRS];
+  for (int j = threadIdx.x; j < a.half; j += blockDim.x) freq[j] = a.freq[j];
+  // this thread's row slot, head and channels
+  const int slot = a.slots == 1 ? 0 : threadIdx.x / a.cols;
+  const int col = blockIdx.y * NT + threadIdx.x - slot * a.cols;
+  const int h = col / a.units, u = col - h * a.units;
+  const bool turned = u < a.pair_units;
+  const int ch = turned ? u * VEC : a.r + (u - a.pair_units) * VEC;
+  const bool is_k = h >= a.Hq;
+  const int64_t si = is_k ? a.sk : a.sq, so = is_k ? a.sok : a.soq;
+  const T* src = is_k ? k + (int64_t)(h - a.Hq) * a.d + ch : q + (int64_t)h * a.d + ch;
+  T* dst = is_k ? ko + (int64_t)(h - a.Hq) * a.d + ch : qo + (int64_t)h * a.d + ch;
+  // in place, the copied channels are there already
+  const bool mine = col < a.cols && (turned || src != dst);
+  const int entry = HALF ? ch : ch / 2;
+  const int rows = a.slots * ROWS_T;  // of a group
+  int side = 0;
+  __syncthreads();
+  for (int64_t row0 = (int64_t)blockIdx.x * rows; row0 < a.n;
+       row0 += (int64_t)gridDim.x * rows, side ^= 1) {
+    const int live = (int)min((int64_t)rows, a.n - row0);
+    V lo[ROWS_T], hi[HALF ? ROWS_T : 1];
+    // loads that wait for nothing (rows that will be left alone are read as well)
 #pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const int h = h0 + i * a.splits;
-      if (h < H && src(h) != dst(h))
-        *reinterpret_cast<V*>(dst(h) + ch) = *reinterpret_cast<const V*>(src(h) + ch);
-    }
-    return;
-  }
-  constexpr int NP = LAYOUT == PACK3D_ROTARY_HALF ? VEC : VEC / 2;  // pairs of a thread
-  const int j0 = u * NP;
-  float cs[NP], sn[NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const uint64_t turn = (uint64_t)p * a.freq[j0 + i];
-    const float x = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
-    sincospif(x, &sn[i], &cs[i]);
-    cs[i] *= a.amp;
-    sn[i] *= a.amp * a.sense;
-  }
-  V lo[HEADS], hi[HEADS];
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i * a.splits;
-    if (h < H) {
-      if (LAYOUT == PACK3D_ROTARY_HALF) {
-        lo[i] = *reinterpret_cast<const V*>(src(h) + j0);
-        hi[i] = *reinterpret_cast<const V*>(src(h) + j0 + a.half);
-      } else {
-        lo[i] = *reinterpret_cast<const V*>(src(h) + 2 * j0);
+    for (int i = 0; i < ROWS_T; ++i) {
+      const int r = slot + i * a.slots;
+      if (mine && r < live) {
+        const T* p = src + (row0 + r) * si;
+        load(lo[i], p);
+        if (HALF && turned) load(hi[HALF ? i : 0], p + a.half);
       }
     }
-  }
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i * a.splits;
-    if (h >= H) continue;
-#pragma unroll
-    for (int e = 0; e < NP; ++e) {
-      T& r1 = LAYOUT == PACK3D_ROTARY_HALF ? lo[i].x[e] : lo[i].x[2 * e];
-      T& r2 = LAYOUT == PACK3D_ROTARY_HALF ? hi[i].x[e] : lo[i].x[2 * e + 1];
-      const float x1 = to_f32<T>(r1), x2 = to_f32<T>(r2);
-      r1 = from_f32<T>(x1 * cs[e] - x2 * sn[e]);
-      r2 = from_f32<T>(x1 * sn[e] + x2 * cs[e]);
+    // (two halves in turn: the barrier below also ends the reads of two groups ago)
+    float2* cs = cs_all + side * rows * a.half;
+    for (int e = threadIdx.x; e < live * a.half; e += blockDim.x) {
+      const int r = e / a.half, j = e - r * a.half;
+      const uint64_t turn = (uint64_t)(int64_t)pos[row0 + r] * freq[j];
+      const float x = (float)(int32_t)(turn >> 32) * 4.656612873077393e-10f;  // 2^-31: half turns
+      float sn, c;
+      sincospif(x, &sn, &c);
+      cs[e] = make_float2(c * a.amp, sn * a.amp * a.sense);
     }
-    if (LAYOUT == PACK3D_ROTARY_HALF) {
-      *reinterpret_cast<V*>(dst(h) + j0) = lo[i];
-      *reinterpret_cast<V*>(dst(h) + j0 + a.half) = hi[i];
-    } else {
-      *reinterpret_cast<V*>(dst(h) + 2 * j0) = lo[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS_T; ++i) {
+      const int r = slot + i * a.slots;
+      // a negative position: behind the last sequence, left as it was
+      if (!mine || r >= live || pos[row0 + r] < 0) continue;
+      T* p = dst + (row0 + r) * so;
+      if (turned) {
+        const float2* c = cs + r * a.half + entry;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) {
+          T& r1 = HALF ? lo[i].x[e] : lo[i].x[2 * e];
+          T& r2 = HALF ? hi[HALF ? i : 0].x[e] : lo[i].x[2 * e + 1];
+          const float x1 = to_f32<T>(r1), x2 = to_f32<T>(r2);
+          r1 = from_f32<T>(x1 * c[e].x - x2 * c[e].y);
+          r2 = from_f32<T>(x1 * c[e].y + x2 * c[e].x);
+        }
+        if (HALF) store(p + a.half, hi[HALF ? i : 0]);
+      }
+      store(p, lo[i]);
     }
   }
 }
@@ -132,23 +163,35 @@ __global__ void __launch_bounds__(NT)
 template <typename T, int VEC, int LAYOUT>
 int launch(RotArgs a, const int32_t* pos, const void* q, const void* k, void* qo, void* ko,
            cudaStream_t s) {
-  const int H = a.Hq + a.Hk;
   a.pair_units = LAYOUT == PACK3D_ROTARY_HALF ? a.half / VEC : a.r / VEC;
   a.units = a.pair_units + (a.d - a.r) / VEC;
-  // Four heads per thread where that still fills the GPU (148 SMs x 2048
-  // threads); one head per thread for few rows, where the length of a thread's
-  // chain is what a call takes.
-  const bool wide = (int64_t)a.n * a.units * H >= (int64_t)148 * 2048 * 4;
-  a.splits = wide ? (H + 3) / 4 : H;
-  const int cols = a.units * a.splits;
-  a.rows = std::max(1, NT / cols);
-  const dim3 grid((unsigned)((a.n + a.rows - 1) / a.rows), (unsigned)((cols + NT - 1) / NT));
+  a.cols = (a.Hq + a.Hk) * a.units;
+  a.slots = std::max(1, NT / a.cols);
+  // Four vectors in flight per thread (two rows in the half layout, whose pairs are
+  // two vectors: 36 against 39 us with four rows at 16,411 x 20 x 128; four rows
+  // interleaved: 75 against 90 us with two at 65,536 x 16 x 96) where that still
+  // gives every SM its 2,048 threads; one row where there are few, and the length
+  // of a thread's chain is what a call takes.
+  constexpr int WIDE = LAYOUT == PACK3D_ROTARY_HALF ? 2 : 4;
+  const bool wide = (int64_t)a.n * a.cols >= (int64_t)148 * 2048 * WIDE;
+  const int rows = wide ? WIDE : 1;
+  // the cosines of two groups fit into the shared memory every block may have
+  a.slots = std::min(a.slots, std::max(1, CS_ENTRIES / (rows * a.half)));
+  const int threads = a.cols < NT ? a.slots * a.cols : NT;
+  const int64_t parts = (a.cols + NT - 1) / NT;
+  // Blocks that stay (sixteen per SM) and walk over groups of rows: a thread's own
+  // frequency comes from the kernel's parameters, which a warp reads one address
+  // at a time, so it is copied to shared memory once per block.
+  const int64_t groups = ((int64_t)a.n + rows * a.slots - 1) / (rows * a.slots);
+  const dim3 grid((unsigned)std::min<int64_t>(groups, std::max<int64_t>(1, 148 * 16 / parts)),
+                  (unsigned)parts);
+  const size_t bytes = 2 * sizeof(float2) * rows * a.slots * a.half;
   if (wide)
-    k_rotary<T, VEC, LAYOUT, 4><<<grid, NT, 0, s>>>(a, pos, (const T*)q, (const T*)k, (T*)qo,
-                                                    (T*)ko);
+    k_rotary<T, VEC, LAYOUT, WIDE><<<grid, threads, bytes, s>>>(
+        a, pos, (const T*)q, (const T*)k, (T*)qo, (T*)ko);
   else
-    k_rotary<T, VEC, LAYOUT, 1><<<grid, NT, 0, s>>>(a, pos, (const T*)q, (const T*)k, (T*)qo,
-                                                    (T*)ko);
+    k_rotary<T, VEC, LAYOUT, 1><<<grid, threads, bytes, s>>>(a, pos, (const T*)q, (const T*)k,
+                                                             (T*)qo, (T*)ko);
   count_launches(1);
   return cuda_status(cudaGetLastError());
 }
@@ -175,43 +218,47 @@ int launch_type(const RotArgs& a, int layout, const int32_t* pos, const void* q,
   }
 }
 
-// theta_j of the r/2 pairs, and the default amplitude of the scaling.
-int frequencies(const pack3d_rotary_params* p, double* theta, double* amp) {
-  const double two_pi = 6.283185307179586476925286766559;
+// theta_j of the r/2 pairs, and the default amplitude of the scaling.  The powers
+// base^(-2j/r) are products of one factor in 64-bit mantissas (128 products are
+// off by 2^-57 at most), which takes a call 1 us less of host time than as many
+// powers.
+int frequencies(const pack3d_rotary_params* p, long double* theta, double* amp) {
+  const long double two_pi = 6.283185307179586476925286766559L;
   const int r = p->rot_dim, half = r / 2;
-  const double f = p->factor;
-  double base = p->base;
+  const long double f = p->factor, L = p->original_length;
+  long double base = p->base;
   *amp = 1.0;
-  if (p->scaling == PACK3D_ROTARY_BASE && r > 2) base *= pow(f, (double)r / (r - 2));
-  for (int j = 0; j < half; ++j) theta[j] = pow(base, -2.0 * j / r);
+  if (p->scaling == PACK3D_ROTARY_BASE && r > 2) base *= powl(f, (long double)r / (r - 2));
+  const long double step = powl(base, -2.0L / r);
+  theta[0] = 1.0L;
+  for (int j = 1; j < half; ++j) theta[j] = theta[j - 1] * step;
   if (p->scaling == PACK3D_ROTARY_LINEAR)
     for (int j = 0; j < half; ++j) theta[j] /= f;
   if (p->scaling == PACK3D_ROTARY_BANDS)
     for (int j = 0; j < half; ++j) {
-      const double turns = p->original_length * theta[j] / two_pi;
-      const double m = std::min(1.0, std::max(0.0, (turns - p->low) / ((double)p->high - p->low)));
-      theta[j] = m * theta[j] + (1.0 - m) * theta[j] / f;
+      const long double turns = L * theta[j] / two_pi;
+      const long double m =
+          std::min(1.0L, std::max(0.0L, (turns - p->low) / ((long double)p->high - p->low)));
+      theta[j] = m * theta[j] + (1.0L - m) * theta[j] / f;
     }
   if (p->scaling == PACK3D_ROTARY_RAMP) {
     auto pair_of = [&](double turns) {
-      return r * log(p->original_length / (two_pi * turns)) / (2.0 * log(base));
+      return r * log(p->original_length / ((double)two_pi * turns)) / (2.0 * log(p->base));
     };
     const double lo = std::max(floor(pair_of(p->high)), 0.0);
     const double hi = std::min(ceil(pair_of(p->low)), (double)(r - 1));
     for (int j = 0; j < half; ++j) {
       const double m = std::min(1.0, std::max(0.0, (j - lo) / std::max(hi - lo, 0.001)));
-      theta[j] = (1.0 - m) * theta[j] + m * theta[j] / f;
+      theta[j] = (1.0L - m) * theta[j] + m * theta[j] / f;
     }
-    *amp = 0.1 * log(f) + 1.0;
+    *amp = 0.1 * log((double)f) + 1.0;
   }
-  for (int j = 0; j < half; ++j)
-    if (!isfinite(theta[j])) return PACK3D_ERR_ARG;
-  return PACK3D_OK;
+  return isfinite(theta[half - 1]) ? PACK3D_OK : PACK3D_ERR_ARG;
 }
 
 int check_params(const pack3d_rotary_params* p) {
   if (!p) return PACK3D_ERR_ARG;
-  if (p->n_tokens < 0 || p->Hq < 1 || p->Hk < 0 || p->Hq > 65536 || p->Hk > 65536)
+  if (p->n_tokens < 0 || p->Hq < 1 || p->Hk < 0 || (int64_t)p->Hq + p->Hk > MAX_HEADS)
     return PACK3D_ERR_ARG;
   if (p->n_tokens > (1 << 30)) return PACK3D_ERR_ARG;
   if (p->head_dim < 1 || p->rot_dim < 2 || (p->rot_dim & 1) || p->rot_dim > p->head_dim)
@@ -246,17 +293,15 @@ int rotary(const pack3d_rotary_params* p, const int32_t* pos, const void* q, con
   int rc = check_params(p);
   if (rc) return rc;
   RotArgs a;
-  double theta[MAX_PAIRS], amp;
+  long double theta[MAX_PAIRS];
+  double amp;
   if ((rc = frequencies(p, theta, &amp))) return rc;
   a.half = p->rot_dim / 2;
-  for (int j = 0; j < MAX_PAIRS; ++j) {
-    long double f = 0.0L;
-    if (j < a.half) {
-      f = (long double)theta[j] / 6.283185307179586476925286766559L;
-      f -= floorl(f);
-    }
-    // 2^64 f, rounded; a fraction that rounds up to 1 is 0 turns
-    const long double x = roundl(ldexpl(f, 64));
+  for (int j = 0; j < a.half; ++j) {
+    // the turn's fraction as 64 bits; one that rounds up to a whole turn is 0
+    long double f = theta[j] * (1.0L / 6.283185307179586476925286766559L);
+    if (f >= 1.0L) f -= floorl(f);
+    const long double x = f * 18446744073709551616.0L + 0.5L;
     a.freq[j] = x >= 18446744073709551616.0L ? 0ull : (uint64_t)x;
   }
   a.amp = p->amplitude > 0.f ? p->amplitude : (float)amp;
@@ -266,7 +311,7 @@ int rotary(const pack3d_rotary_params* p, const int32_t* pos, const void* q, con
   a.n = p->n_tokens;
   a.Hq = p->Hq;
   a.Hk = p->Hk;
-  a.units = a.pair_units = a.splits = a.rows = 0;
+  a.units = a.pair_units = a.cols = a.slots = 0;
   const int64_t cq = (int64_t)p->Hq * p->head_dim, ck = (int64_t)p->Hk * p->head_dim;
   a.sq = p->stride_q ? p->stride_q : cq;
   a.sk = p->stride_k ? p->stride_k : ck;

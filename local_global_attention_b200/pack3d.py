@@ -483,6 +483,11 @@ _DTYPES = {"bf16": BF16, "fp32": FP32, torch.bfloat16: BF16, torch.float32: FP32
 _TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
 
 
+def _raw_stream(device_index):
+    """The current stream of a device, without a Stream object around it."""
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
 def make_seq_params(n_seqs: int, n_tokens: int, heads: int, kv_heads: int = None,
                     head_dim: int = 96, causal: bool = True, dtype="bf16",
                     scale: float = 0.0) -> SeqParams:
@@ -513,19 +518,21 @@ class _Launch:
     device) or the device's current one.  Buffers allocated here are recorded on
     a given stream, so that the allocator does not hand them on early."""
 
+    __slots__ = ("device", "given", "raw", "before")
+
     def __init__(self, like, stream):
-        if not like.is_cuda:
+        dev = like.device
+        if dev.type != "cuda":
             raise ValueError("PACK3D tensors must be CUDA tensors")
-        self.device, self.given = like.device, None
+        self.device, self.given, self.before = dev, None, None
         if stream is None:
-            self.raw = torch.cuda.current_stream(self.device).cuda_stream
+            self.raw = _raw_stream(dev.index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-            if stream.device != self.device:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {self.device}")
+                stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
             self.given, self.raw = stream, stream.cuda_stream
-        self.before = None
 
     def __enter__(self):
         now = torch.cuda.current_device()
@@ -540,16 +547,15 @@ class _Launch:
 
     def rows(self, t, shape, dtype, what):
         """The token stride of a [rows, heads, head_dim] tensor whose heads and
-        channels lie without gaps."""
-        if t.device != self.device:
-            raise ValueError(f"{what} is on {t.device}, not on {self.device}")
-        if t.dtype != dtype:
-            raise ValueError(f"{what} is {t.dtype}, not {dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        channels lie without gaps (0: nor its tokens)."""
+        if t.device != self.device or t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{what} must be a {dtype} tensor {tuple(shape)} on {self.device}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+        if t.is_contiguous():
+            return 0
         n, h, d = shape
         s = t.stride()
-        if n * h * d and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
             raise ValueError(f"{what}: the heads and channels of a token must be contiguous")
         if n <= 1:
             return 0
@@ -565,7 +571,14 @@ class _Launch:
                              f"{self.device}")
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
+        return self._kept(torch.empty(shape, dtype=dtype, device=self.device))
+
+    def like(self, t, shape):
+        """An empty tensor without gaps in the shape and type of t (the quickest way
+        to one: the smallest calls spend most of their time on the host)."""
+        return self._kept(torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape))
+
+    def _kept(self, t):
         if self.given is not None:
             t.record_stream(self.given)
         return t
@@ -640,7 +653,7 @@ def pack3d_seq_forward(params: SeqParams, index: SeqIndex, q, k, v, out=None, ls
         st = SeqStrides(q=at.rows(q, qs, dt, "q"), k=at.rows(k, ks, dt, "k"),
                         v=at.rows(v, ks, dt, "v"))
         if out is None:
-            out = at.empty(qs, dt)
+            out = at.like(q, qs)
         else:
             st.out = at.rows(out, qs, dt, "out")
         if lse is None:
@@ -667,15 +680,15 @@ def pack3d_seq_backward(params: SeqParams, index: SeqIndex, q, k, v, out, lse, d
                         dout=at.rows(dout, qs, dt, "dout"))
         at.flat(lse, ls, torch.float32, "lse")
         if dq is None:
-            dq = at.empty(qs, dt)
+            dq = at.like(q, qs)
         else:
             st.dq = at.rows(dq, qs, dt, "dq")
         if dk is None:
-            dk = at.empty(ks, dt)
+            dk = at.like(k, ks)
         else:
             st.dk = at.rows(dk, ks, dt, "dk")
         if dv is None:
-            dv = at.empty(ks, dt)
+            dv = at.like(v, ks)
         else:
             st.dv = at.rows(dv, ks, dt, "dv")
         if workspace is None:
@@ -702,14 +715,14 @@ def _rotary(name, params, positions, q, k, q_out, k_out, stream):
         p.n_tokens, p.Hq, p.Hk = n, q.shape[1], 0
         p.stride_q = at.rows(q, qs, dt, "q")
         if q_out is None:
-            q_out = at.empty(qs, dt)
+            q_out = at.like(q, qs)
         else:
             p.stride_q_out = at.rows(q_out, qs, dt, "q_out")
         if k is not None:
             ks = (n, k.shape[1], d)
             p.Hk, p.stride_k = k.shape[1], at.rows(k, ks, dt, "k")
             if k_out is None:
-                k_out = at.empty(ks, dt)
+                k_out = at.like(k, ks)
             else:
                 p.stride_k_out = at.rows(k_out, ks, dt, "k_out")
         _check(getattr(load(), name)(p, positions.data_ptr(), q.data_ptr(),

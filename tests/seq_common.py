@@ -18,6 +18,7 @@ The bounds are sums of these terms per value, nothing is fitted.
 """
 import math
 
+import numpy as np
 import torch
 
 TYPES = {"bf16": (torch.bfloat16, 2.0 ** -8), "fp32": (torch.float32, 2.0 ** -24)}
@@ -109,24 +110,35 @@ def within(got, value, bound, what):
 
 
 def frequencies(r, base, scaling="none", factor=1.0, length=0, low=0.0, high=0.0):
-    """theta_j of a rotary scaling, and its amplitude."""
-    th = torch.tensor([float(base)] * (r // 2), dtype=torch.float64)
-    if scaling == "base" and r > 2:
-        th = th * factor ** (r / (r - 2))
-    j = torch.arange(r // 2, dtype=torch.float64)
-    th = th ** (-2 * j / r)
+    """theta_j of a rotary scaling, and its amplitude.  The tensor carries theta_j in
+    64-bit mantissas too (attribute `ld`): at position 2^31 half a step of a
+    double theta is 2^-22 of a radian already, as large as the fp32 bounds."""
+    ld, two_pi = np.longdouble, 2 * np.arccos(np.longdouble(-1))
+    j = np.arange(r // 2)
+    b = ld(base) * (ld(factor) ** (ld(r) / ld(r - 2)) if scaling == "base" and r > 2 else ld(1))
+    th, amp = b ** (-2 * j.astype(ld) / ld(r)), 1.0
     if scaling == "linear":
-        return th / factor, 1.0
+        th = th / ld(factor)
     if scaling == "bands":
-        w = ((length * th / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
-        return w * th + (1 - w) * th / factor, 1.0
+        w = np.clip((length * th / two_pi - ld(low)) / (ld(high) - ld(low)), ld(0), ld(1))
+        th = w * th + (1 - w) * th / ld(factor)
     if scaling == "ramp":
         def pair(turns):
             return r * math.log(length / (2 * math.pi * turns)) / (2 * math.log(base))
         lo, hi = max(math.floor(pair(high)), 0), min(math.ceil(pair(low)), r - 1)
-        w = ((j - lo) / max(hi - lo, 0.001)).clamp(0, 1)
-        return (1 - w) * th + w * th / factor, 0.1 * math.log(factor) + 1
-    return th, 1.0
+        w = np.clip((j.astype(ld) - lo) / ld(max(hi - lo, 0.001)), ld(0), ld(1))
+        th, amp = (1 - w) * th + w * th / ld(factor), 0.1 * math.log(factor) + 1
+    out = torch.from_numpy(th.astype(np.float64))
+    out.ld = th
+    return out, amp
+
+
+def angles(positions, th):
+    """position * theta_j modulo a turn, to 2^-30 of a radian at any position."""
+    two_pi = 2 * np.arccos(np.longdouble(-1))
+    a = positions.cpu().numpy().astype(np.longdouble)[:, None] * th.ld
+    a = a - two_pi * np.floor(a / two_pi)
+    return torch.from_numpy(a.astype(np.float64)).to(positions.device)
 
 
 def rotated(x, positions, th, amp, layout, sense=1.0):
@@ -137,7 +149,7 @@ def rotated(x, positions, th, amp, layout, sense=1.0):
     2^-24 of a (|x1| + |x2|) cover them; then the output's rounding."""
     u = 2.0 ** -8 if x.dtype == torch.bfloat16 else 2.0 ** -24
     r = 2 * th.numel()
-    ang = positions.double()[:, None, None] * th.to(x.device)
+    ang = angles(positions, th)[:, None]
     c, s = amp * ang.cos(), sense * amp * ang.sin()
     y = x.double()
     i1, i2 = (slice(0, r // 2), slice(r // 2, r)) if layout == "half" else \
