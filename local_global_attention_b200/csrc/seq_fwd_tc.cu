@@ -39,7 +39,7 @@ namespace seq {
 
 namespace {
 
-constexpr int MMA_WARP = 8, TMA_WARP = 9, NT = 320;
+constexpr int MMA_WARP = 8, TMA_WARP = 9, NT = 384;
 constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;
 constexpr float RESCALE_THRESHOLD = 8.0f;
 
@@ -137,6 +137,8 @@ __global__ void __launch_bounds__(NT, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
 
+  if (warp >= 8) {
+    regs_dec<OTHER_REGS>();
   if (warp == TMA_WARP) {
     // ================= TMA producer (lane 0) =================
     const int hk = h / g.G, row0 = t.start + t.off;
@@ -234,7 +236,9 @@ __global__ void __launch_bounds__(NT, 1)
       if (j + 1 < n) mma_commit_warp(&sm.empty[(2 * j + 2) % NST]);
     }
     __syncwarp();
+  }
   } else {
+    regs_inc<ARITH_REGS>();
     // ================= softmax (one query row per thread) =================
     const int i = warp >> 2, ni = i ? n1 : n0;
     const int r = tid & (ROWS - 1);

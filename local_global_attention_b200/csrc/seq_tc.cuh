@@ -43,6 +43,20 @@ __host__ __device__ constexpr uint32_t k_step(int st) {
 }
 __host__ __device__ constexpr uint32_t row_step(int st) { return (uint32_t)(st * 16 * 128) >> 4; }
 
+// Move registers between warpgroups (all four warps of one execute the same
+// call): the kernel is launched with 168 registers per thread, 384 threads; two
+// warpgroups take ARITH_REGS each, the third keeps OTHER_REGS.
+constexpr int ARITH_REGS = 208, OTHER_REGS = 80;
+static_assert(2 * ARITH_REGS + OTHER_REGS <= 3 * 168, "registers of the launch");
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // A wait of a whole converged warp.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
                                           volatile int32_t* abort) {
