@@ -111,10 +111,9 @@ __global__ void __launch_bounds__(NT, 1)
              __nv_bfloat16* __restrict__ dq) {
   using C = Cfg<HD>;
   constexpr int NSEG = C::NSEG, NST = C::NST;
-  if (ix.err[0]) return;
   const int h = blockIdx.x % g.Hq;
-  const Tile t = reinterpret_cast<const Tile*>(ix.query)[blockIdx.x / g.Hq];
-  if (t.len == 0) return;
+  const Tile t = load_tile_entry(ix.query, blockIdx.x / g.Hq);
+  if (ix.err[0] || t.len == 0) return;
   extern __shared__ uint8_t smem_raw[];
   SmemQ<HD>& sm = *reinterpret_cast<SmemQ<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~(uintptr_t)1023);
@@ -139,6 +138,12 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_barrier_init();
+  }
+  if (warp == TMA_WARP && lane == 0) {
+    tma_prefetch_map(&maps.q);
+    tma_prefetch_map(&maps.k);
+    tma_prefetch_map(&maps.v);
+    tma_prefetch_map(&maps.dout);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(&sm.tmem_base, TMEM_COLS);
@@ -393,10 +398,9 @@ __global__ void __launch_bounds__(NT, 1)
   using C = Cfg<HD>;
   constexpr int NSEG = C::NSEG, NST = C::NSTK;
   constexpr uint32_t KCOL_DV = KCOL_DK + HD;
-  if (ix.err[0]) return;
   const int hk = blockIdx.x % g.Hk;
-  const Tile t = reinterpret_cast<const Tile*>(ix.key)[blockIdx.x / g.Hk];
-  if (t.len == 0) return;
+  const Tile t = load_tile_entry(ix.key, blockIdx.x / g.Hk);
+  if (ix.err[0] || t.len == 0) return;
   extern __shared__ uint8_t smem_raw[];
   SmemK<HD>& sm = *reinterpret_cast<SmemK<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~(uintptr_t)1023);
@@ -424,6 +428,12 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_barrier_init();
+  }
+  if (warp == TMA_WARP && lane == 0) {
+    tma_prefetch_map(&maps.q);
+    tma_prefetch_map(&maps.k);
+    tma_prefetch_map(&maps.v);
+    tma_prefetch_map(&maps.dout);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(&sm.tmem_base, TMEM_COLS);

@@ -36,6 +36,11 @@ struct Tile {
   int start, len, off, pad;
 };
 
+__device__ __forceinline__ Tile load_tile_entry(const int32_t* list, int i) {
+  const int4 x = __ldg(reinterpret_cast<const int4*>(list) + i);
+  return Tile{x.x, x.y, x.z, x.w};
+}
+
 int make_geo(const pack3d_seq_params* p, SeqGeo* g);
 int make_strides(const SeqGeo& g, const pack3d_seq_strides* s, Strides* out);
 

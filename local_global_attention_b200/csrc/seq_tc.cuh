@@ -72,6 +72,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity,
   return false;
 }
 
+// Maximum of three values in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Rows [from, ROWS) of a tile set to zero by one warp, visible to the tensor
 // core once the warp has arrived on a barrier: what stands behind the last row
 // of a sequence (the next sequence, or anything) must not enter a product that

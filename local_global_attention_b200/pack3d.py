@@ -483,11 +483,6 @@ _DTYPES = {"bf16": BF16, "fp32": FP32, torch.bfloat16: BF16, torch.float32: FP32
 _TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
 
 
-def _raw_stream(device_index):
-    """The current stream of a device, without a Stream object around it."""
-    return torch._C._cuda_getCurrentRawStream(device_index)
-
-
 def make_seq_params(n_seqs: int, n_tokens: int, heads: int, kv_heads: int = None,
                     head_dim: int = 96, causal: bool = True, dtype="bf16",
                     scale: float = 0.0) -> SeqParams:
@@ -518,27 +513,26 @@ class _Launch:
     device) or the device's current one.  Buffers allocated here are recorded on
     a given stream, so that the allocator does not hand them on early."""
 
-    __slots__ = ("device", "given", "raw", "before")
+    __slots__ = ("index", "given", "raw", "before")
 
     def __init__(self, like, stream):
-        dev = like.device
-        if dev.type != "cuda":
+        self.index = index = like.get_device()
+        if index < 0:
             raise ValueError("PACK3D tensors must be CUDA tensors")
-        self.device, self.given, self.before = dev, None, None
         if stream is None:
-            self.raw = _raw_stream(dev.index)
+            self.given, self.raw = None, torch._C._cuda_getCurrentRawStream(index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=dev)
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            if stream.device.index != index:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
             self.given, self.raw = stream, stream.cuda_stream
 
     def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.device.index:
-            self.before = now
-            torch.cuda.set_device(self.device)
+        now = torch._C._cuda_getDevice()
+        self.before = None if now == self.index else now
+        if self.before is not None:
+            torch.cuda.set_device(self.index)
         return self
 
     def __exit__(self, *exc):
@@ -548,8 +542,8 @@ class _Launch:
     def rows(self, t, shape, dtype, what):
         """The token stride of a [rows, heads, head_dim] tensor whose heads and
         channels lie without gaps (0: nor its tokens)."""
-        if t.device != self.device or t.dtype != dtype or t.shape != shape:
-            raise ValueError(f"{what} must be a {dtype} tensor {tuple(shape)} on {self.device}, "
+        if t.get_device() != self.index or t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{what} must be a {dtype} tensor {tuple(shape)} on cuda:{self.index}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
         if t.is_contiguous():
             return 0
@@ -565,20 +559,17 @@ class _Launch:
         return s[0]
 
     def flat(self, t, shape, dtype, what):
-        if t.device != self.device or t.dtype != dtype or t.shape != shape or \
+        if t.get_device() != self.index or t.dtype is not dtype or t.shape != shape or \
                 not t.is_contiguous():
             raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on "
-                             f"{self.device}")
-
-    def empty(self, shape, dtype):
-        return self._kept(torch.empty(shape, dtype=dtype, device=self.device))
+                             f"cuda:{self.index}")
 
     def like(self, t, shape):
         """An empty tensor without gaps in the shape and type of t (the quickest way
         to one: the smallest calls spend most of their time on the host)."""
-        return self._kept(torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape))
+        return self.kept(torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape))
 
-    def _kept(self, t):
+    def kept(self, t):
         if self.given is not None:
             t.record_stream(self.given)
         return t
@@ -594,6 +585,7 @@ class SeqIndex:
             raise Pack3dError(ERR_ARG, "pack3d_seq_index_bytes")
         self.params = params
         self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        self.device = self.buffer.get_device()
         self.struct = SeqIndexStruct()
         base = self.buffer.data_ptr()
         _check(lib.pack3d_seq_index_init(ctypes.byref(params), base + (-base) % 256, nbytes,
@@ -620,11 +612,10 @@ def pack3d_seq_build_index(params: SeqParams, cu_seqlens: torch.Tensor, index: S
     with _Launch(cu_seqlens, stream) as at:
         at.flat(cu_seqlens, (params.n_seqs + 1,), torch.int32, "cu_seqlens")
         if index is None:
-            index = SeqIndex(params, device=at.device)
-            if at.given is not None:
-                index.buffer.record_stream(at.given)
-        elif index.buffer.device != at.device:
-            raise ValueError(f"the index is on {index.buffer.device}, not on {at.device}")
+            index = SeqIndex(params, device=cu_seqlens.device)
+            at.kept(index.buffer)
+        elif index.device != at.index:
+            raise ValueError(f"the index is on cuda:{index.device}, not on cuda:{at.index}")
         _check(load().pack3d_seq_build_index(params, cu_seqlens.data_ptr(), index.struct, at.raw),
                "pack3d_seq_build_index")
     return index
@@ -637,8 +628,8 @@ def pack3d_seq_index_check(index: SeqIndex, stream=None) -> int:
 
 
 def _seq_call(params, index, at):
-    if index.buffer.device != at.device:
-        raise ValueError(f"the index is on {index.buffer.device}, not on {at.device}")
+    if index.device != at.index:
+        raise ValueError(f"the index is on cuda:{index.device}, not on cuda:{at.index}")
     n, d, dt = params.n_tokens, params.head_dim, _TORCH_DTYPE[params.dtype]
     return (n, params.Hq, d), (n, params.Hk, d), (params.Hq, n), dt
 
@@ -657,7 +648,7 @@ def pack3d_seq_forward(params: SeqParams, index: SeqIndex, q, k, v, out=None, ls
         else:
             st.out = at.rows(out, qs, dt, "out")
         if lse is None:
-            lse = at.empty(ls, torch.float32)
+            lse = at.kept(q.new_empty(ls, dtype=torch.float32))
         else:
             at.flat(lse, ls, torch.float32, "lse")
         _check(load().pack3d_seq_forward(params, index.struct, st, q.data_ptr(), k.data_ptr(),
@@ -692,9 +683,10 @@ def pack3d_seq_backward(params: SeqParams, index: SeqIndex, q, k, v, out, lse, d
         else:
             st.dv = at.rows(dv, ks, dt, "dv")
         if workspace is None:
-            workspace = at.empty((pack3d_seq_backward_workspace_bytes(params),), torch.uint8)
-        elif workspace.device != at.device or not workspace.is_contiguous():
-            raise ValueError(f"the workspace must be a contiguous tensor on {at.device}")
+            workspace = at.kept(q.new_empty(pack3d_seq_backward_workspace_bytes(params),
+                                            dtype=torch.uint8))
+        elif workspace.get_device() != at.index or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be a contiguous tensor on cuda:{at.index}")
         _check(load().pack3d_seq_backward(params, index.struct, st, q.data_ptr(), k.data_ptr(),
                                           v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                           dout.data_ptr(), dq.data_ptr(), dk.data_ptr(),
