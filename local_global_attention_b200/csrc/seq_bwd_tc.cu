@@ -39,7 +39,7 @@ namespace seq {
 
 namespace {
 
-constexpr int MMA_WARP = 8, TMA_WARP = 9, STAT_WARP = 10, NT = 384, EW = 256;
+constexpr int MMA_WARP = 8, TMA_WARP = 9, STAT_WARP = 10, NT = 384;
 constexpr uint32_t TMEM_COLS = 512;
 
 template <int HD>
@@ -61,23 +61,20 @@ __device__ __forceinline__ void bar_elementwise() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// One row of an accumulator, scaled and rounded: channels [c0, c0 + 16) of 16
-// columns at taddr, to dst (the row's first channel), channels below d.
-__device__ __forceinline__ void store_cols16(uint32_t taddr, float f, __nv_bfloat16* dst, int c0,
-                                             int d, bool write) {
-  uint32_t o[16];
-  tmem_ld16(taddr, o);
-  tmem_wait_ld();
-  if (!write) return;
+// Half `half` of the HD channels of a warp's 32 accumulator rows (HD / 2 is no
+// multiple of 32 at 96: that half overlaps the other's last 16 channels, and the
+// same values are stored twice).
+template <int HD>
+__device__ __forceinline__ void store_acc(uint32_t taddr, float f, __nv_bfloat16* dst,
+                                          int64_t stride, int live, int half, int d, int lane) {
+  constexpr int N = (HD / 2 + 31) / 32;  // pieces of 32 channels
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    if (c0 + 8 * e >= d) break;
-    uint32_t w[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      w[x] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * x]) * f,
-                         __uint_as_float(o[8 * e + 2 * x + 1]) * f);
-    *reinterpret_cast<uint4*>(dst + c0 + 8 * e) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int c = 0; c < N; ++c) {
+    const int c0 = half ? HD - 32 * (c + 1) : 32 * c;
+    uint32_t o[32];
+    tmem_ld32(taddr + c0, o);
+    tmem_wait_ld();
+    store_rows32(o, f, dst, stride, live, c0, d, lane);
   }
 }
 
@@ -349,12 +346,10 @@ __global__ void __launch_bounds__(NT, 1)
     if (ok) ok = warp_wait(&sm.done, 0, abort_flag);
     if (ok) {
       tc_fence_after();
-      __nv_bfloat16* dst = dq + row * st.dq + (int64_t)h * g.d;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        const int c0 = half * (HD / 2) + 16 * c;
-        store_cols16(tbase + lane_base + QCOL_ACC + c0, g.tau, dst, c0, g.d, live);
-      }
+      const int base = pos - lane;  // the warp's first row
+      store_acc<HD>(tbase + lane_base + QCOL_ACC, g.tau,
+                    dq + ((int64_t)t.start + base) * st.dq + (int64_t)h * g.d, st.dq, t.len - base,
+                    half, g.d, lane);
     }
   }
 
@@ -620,16 +615,12 @@ __global__ void __launch_bounds__(NT, 1)
     if (ok) ok = warp_wait(&sm.done, 0, abort_flag);
     if (ok) {
       tc_fence_after();
-      const bool live = pos < t.len;
-      const int64_t row = (int64_t)t.start + pos;
-      __nv_bfloat16* to_k = dk + row * st.dk + (int64_t)hk * g.d;
-      __nv_bfloat16* to_v = dv + row * st.dv + (int64_t)hk * g.d;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
-        const int c0 = half * (HD / 2) + 16 * c;
-        store_cols16(tbase + lane_base + KCOL_DK + c0, g.tau, to_k, c0, g.d, live);
-        store_cols16(tbase + lane_base + KCOL_DV + c0, 1.f, to_v, c0, g.d, live);
-      }
+      const int base = pos - lane;  // the warp's first row
+      const int64_t row = (int64_t)t.start + base;
+      store_acc<HD>(tbase + lane_base + KCOL_DK, g.tau, dk + row * st.dk + (int64_t)hk * g.d, st.dk,
+                    t.len - base, half, g.d, lane);
+      store_acc<HD>(tbase + lane_base + KCOL_DV, 1.f, dv + row * st.dv + (int64_t)hk * g.d, st.dv,
+                    t.len - base, half, g.d, lane);
     }
   }
 

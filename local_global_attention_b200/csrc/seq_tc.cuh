@@ -93,6 +93,52 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
   __syncwarp();
 }
 
+// 32 channels [c0, c0 + 32) of a warp's 32 accumulator rows (lane = row), scaled
+// and rounded to bf16, into rows `stride` elements apart from dst on: rows below
+// `live`, channels below d.  Four lanes first exchange their 16-byte pieces, so
+// that they store 64 contiguous bytes of one row: an access of a warp then meets 8
+// lines instead of 32 (an epilogue of 128 channels took 2,600 cycles with a row
+// per lane).
+__device__ __forceinline__ void store_rows32(const uint32_t (&o)[32], float f, __nv_bfloat16* dst,
+                                             int64_t stride, int live, int c0, int d, int lane) {
+  uint32_t w[4][4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float2 y = f2_mul(make_float2(__uint_as_float(o[8 * c + 2 * x]),
+                                          __uint_as_float(o[8 * c + 2 * x + 1])),
+                              make_float2(f, f));
+      w[c][x] = pack_bf16x2(y.x, y.y);
+    }
+  // transpose (lane of the four) x (piece), one bit at a time
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit *= 2) {
+    const bool upper = lane & bit;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c & bit) continue;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t got =
+            __shfl_xor_sync(0xffffffffu, upper ? w[c][x] : w[c | bit][x], bit);
+        if (upper)
+          w[c][x] = got;
+        else
+          w[c | bit][x] = got;
+      }
+    }
+  }
+  const int ch = c0 + 8 * (lane & 3);
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int row = (lane & ~3) + s;
+    if (row < live && ch < d)
+      *reinterpret_cast<uint4*>(dst + row * stride + ch) =
+          make_uint4(w[s][0], w[s][1], w[s][2], w[s][3]);
+  }
+}
+
 // Tensor map of a packed tensor [N][H][d] (tokens `stride` elements apart):
 // boxes of {64 channels, 1 head, `rows` rows}.
 inline bool encode_rows(CUtensorMap* m, const void* base, int d, int H, int N, int64_t stride,
