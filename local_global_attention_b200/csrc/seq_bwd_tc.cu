@@ -86,6 +86,7 @@ struct SmemQ {
   uint8_t kv[Cfg<HD>::NST][Cfg<HD>::TILE];  // ring: k_0, v_0, k_1, v_1, ...
   float part[2][ROWS];                      // halves of row sums
   uint64_t q_full, do_full;
+  uint64_t o_full, o_read;  // out in the ring's last slot, before that is a ring slot
   uint64_t full[Cfg<HD>::NST], empty[Cfg<HD>::NST];
   uint64_t s_full[2], dp_full, ds_full;
   uint64_t k_fixed, done, drain;
@@ -94,7 +95,7 @@ struct SmemQ {
 };
 
 struct MapsB {
-  CUtensorMap q, k, v, dout;
+  CUtensorMap q, k, v, dout, out;
 };
 
 // Tensor memory: S (two buffers, dS over the columns read), dP, dq.
@@ -103,7 +104,6 @@ constexpr uint32_t QCOL_S = 0, QCOL_DP = 256, QCOL_ACC = 384;
 template <int HD>
 __global__ void __launch_bounds__(NT, 1)
     k_seq_dq(SeqGeo g, Strides st, pack3d_seq_index ix, const __grid_constant__ MapsB maps,
-             const __nv_bfloat16* __restrict__ out, const __nv_bfloat16* __restrict__ dout,
              const float* __restrict__ lse, float* __restrict__ delta, float* __restrict__ lse2,
              __nv_bfloat16* __restrict__ dq) {
   using C = Cfg<HD>;
@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(NT, 1)
   if (tid == 0) {
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.do_full, 1);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_read, 8);  // one arrival per elementwise warp
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(NT, 1)
     tma_prefetch_map(&maps.k);
     tma_prefetch_map(&maps.v);
     tma_prefetch_map(&maps.dout);
+    tma_prefetch_map(&maps.out);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(&sm.tmem_base, TMEM_COLS);
@@ -163,12 +166,18 @@ __global__ void __launch_bounds__(NT, 1)
         if (round > 0 &&
             !(ok = mbar_wait_or_abort(&sm.empty[s], (round - 1) & 1, WAIT_LIMIT, abort_flag)))
           break;
+        if (i == NST - 1 && !(ok = mbar_wait_or_abort(&sm.o_read, 0, WAIT_LIMIT, abort_flag)))
+          break;
         mbar_arrive_expect_tx(&sm.full[s], C::TILE);
         load_tile_tma<NSEG>(sm.kv[s], (i & 1) ? &maps.v : &maps.k, hk, t.start + (i / 2) * ROWS,
                             &sm.full[s]);
         if (i == 0) {
           mbar_arrive_expect_tx(&sm.do_full, C::TILE);
           load_tile_tma<NSEG>(sm.dout, &maps.dout, h, row0, &sm.do_full);
+          if (n > 1) {
+            mbar_arrive_expect_tx(&sm.o_full, C::TILE);
+            load_tile_tma<NSEG>(sm.kv[NST - 1], &maps.out, h, row0, &sm.o_full);
+          }
         }
         issued = i + 1;
       }
@@ -185,6 +194,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (lane == 0) {  // copies in flight land before the CTA ends (bounded)
       mbar_wait(&sm.q_full, 0, WAIT_LIMIT);
       if (issued > 0) mbar_wait(&sm.do_full, 0, WAIT_LIMIT);
+      if (issued > 0 && n > 1) mbar_wait(&sm.o_full, 0, WAIT_LIMIT);
       for (int i = max(0, issued - NST); i < issued; ++i)
         mbar_wait(&sm.full[i % NST], (i / NST) & 1, WAIT_LIMIT);
     }
@@ -247,31 +257,35 @@ __global__ void __launch_bounds__(NT, 1)
     const float c2 = g.tau * LOG2E;
     const float L = live ? lse[(int64_t)h * g.N + row] * LOG2E : 0.f;
     float dl = 0.f;
+    bool ok = true;
     if (n > 1) {
-      // delta = dout . out, half the channels per thread
-      const int chunks = g.d / 8, first = half * ((chunks + 1) / 2),
-                last = half ? chunks : (chunks + 1) / 2;
+      // delta = dout . out from shared memory, half the channels per thread (16-byte
+      // piece c of row r stands at c ^ (r % 8): no bank conflicts).  Read from global
+      // memory the two tiles took 8,000 cycles, past the little L1 cache that the
+      // shared memory leaves.
+      ok = warp_wait(&sm.do_full, 0, abort_flag) && warp_wait(&sm.o_full, 0, abort_flag);
       float x = 0.f;
-      if (live) {
-        const uint4* a = reinterpret_cast<const uint4*>(out + row * st.out + (int64_t)h * g.d);
-        const uint4* b = reinterpret_cast<const uint4*>(dout + row * st.dout + (int64_t)h * g.d);
-        for (int c = first; c < last; ++c) {
-          const uint4 u = a[c], w = b[c];
-          const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 y = unpack_bf16x2(uu[e]), z = unpack_bf16x2(ww[e]);
-            x = fmaf(y.x, z.x, x);
-            x = fmaf(y.y, z.y, x);
-          }
+      for (int c = 0; c < HD / 16; ++c) {
+        const int ch = half * (HD / 16) + c;
+        const uint32_t at = (ch >> 3) * SEG + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        const uint4 u = *reinterpret_cast<const uint4*>(sm.kv[NST - 1] + at);
+        const uint4 w = *reinterpret_cast<const uint4*>(sm.dout + at);
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = unpack_bf16x2(uu[e]), z = unpack_bf16x2(ww[e]);
+          x = fmaf(y.x, z.x, x);
+          x = fmaf(y.y, z.y, x);
         }
       }
       sm.part[half][r] = x;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.o_read);
       bar_elementwise();
       dl = sm.part[0][r] + sm.part[1][r];
     }
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    for (int j = 0; j < n && ok; ++j) {
       const uint32_t tS = tbase + lane_base + QCOL_S + ROWS * (j & 1) + 64 * half;
       const uint32_t tP = tbase + lane_base + QCOL_DP + 64 * half;
       if (!(ok = warp_wait(&sm.s_full[j & 1], (j >> 1) & 1, abort_flag))) break;
@@ -373,7 +387,7 @@ template <int HD>
 struct SmemK {
   uint8_t k[Cfg<HD>::TILE], v[Cfg<HD>::TILE];
   uint8_t qd[Cfg<HD>::NSTK][Cfg<HD>::TILE];  // ring: q_0, dout_0, q_1, dout_1, ...
-  float stat[Cfg<HD>::NSTK][2][ROWS];       // L and delta of the query tile in the slot
+  alignas(16) float stat[Cfg<HD>::NSTK][2][ROWS];  // L and delta of the query tile in the slot
   uint64_t k_full, v_full;
   uint64_t full[Cfg<HD>::NSTK], ready[Cfg<HD>::NSTK], empty[Cfg<HD>::NSTK];
   uint64_t s_full, dp_full, p_full, ds_full;
@@ -439,6 +453,8 @@ __global__ void __launch_bounds__(NT, 1)
   tc_fence_after();
   const uint32_t tbase = sm.tmem_base;
 
+  if (warp >= 8) {
+    regs_dec<OTHER_REGS>();
   if (warp == TMA_WARP) {
     int issued = 0;
     if (lane == 0) {
@@ -549,7 +565,9 @@ __global__ void __launch_bounds__(NT, 1)
         mma_commit_warp(&sm.done);
     }
     __syncwarp();
-  } else if (warp < 8) {
+  }
+  } else {
+    regs_inc<ARITH_REGS>();
     const int half = warp >> 2, r = tid & (ROWS - 1);
     const int pos = t.off + r;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -562,8 +580,10 @@ __global__ void __launch_bounds__(NT, 1)
     for (int i = 0; i < n; ++i) {
       const int s = (2 * i) % NST;
       if (!(ok = warp_wait(&sm.ready[s], ((2 * i) / NST) & 1, abort_flag))) break;
-      const float2* L = reinterpret_cast<const float2*>(sm.stat[s][0] + 64 * half);
-      const float2* D = reinterpret_cast<const float2*>(sm.stat[s][1] + 64 * half);
+      const float4* stat = reinterpret_cast<const float4*>(sm.stat[s][0] + 64 * half);
+      float4 v[16];  // -L, then -delta of this half's columns
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = stat[e];
       if (!(ok = warp_wait(&sm.s_full, i & 1, abort_flag))) break;
       tc_fence_after();
       uint32_t x[64], p[32];
@@ -574,7 +594,8 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
         const float2 y = f2_fma(
-            make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), cc, L[e]);
+            make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), cc,
+            e & 1 ? make_float2(v[e / 2].z, v[e / 2].w) : make_float2(v[e / 2].x, v[e / 2].y));
         x[2 * e] = __float_as_uint(ex2(y.x));
         x[2 * e + 1] = __float_as_uint(ex2(y.y));
       }
@@ -592,6 +613,8 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = stat[ROWS / 4 + e];
       if (!(ok = warp_wait(&sm.dp_full, i & 1, abort_flag))) break;
       tc_fence_after();
       uint32_t y[64];
@@ -601,8 +624,9 @@ __global__ void __launch_bounds__(NT, 1)
       tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        float2 z = f2_add(make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
-                          D[e]);
+        float2 z = f2_add(
+            make_float2(__uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1])),
+            e & 1 ? make_float2(v[e / 2].z, v[e / 2].w) : make_float2(v[e / 2].x, v[e / 2].y));
         z = f2_mul(z, make_float2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])));
         p[e] = pack_bf16x2(z.x, z.y);
       }
@@ -646,7 +670,8 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
   if (!encode_rows(&maps.q, q, g.d, g.Hq, g.N, st.q, ROWS) ||
       !encode_rows(&maps.k, k, g.d, g.Hk, g.N, st.k, ROWS) ||
       !encode_rows(&maps.v, v, g.d, g.Hk, g.N, st.v, ROWS) ||
-      !encode_rows(&maps.dout, dout, g.d, g.Hq, g.N, st.dout, ROWS))
+      !encode_rows(&maps.dout, dout, g.d, g.Hq, g.N, st.dout, ROWS) ||
+      !encode_rows(&maps.out, out, g.d, g.Hq, g.N, st.out, ROWS))
     return PACK3D_ERR_CUDA;
   constexpr size_t bq = sizeof(SmemQ<HD>) + 1024, bk = sizeof(SmemK<HD>) + 1024;
   static_assert(bq <= 232448 && bk <= 232448, "shared memory of a CTA");
@@ -657,7 +682,7 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
     return PACK3D_ERR_CUDA;
   using B = __nv_bfloat16;
   k_seq_dq<HD><<<(unsigned)(g.n_rows * g.Hq), NT, bq, s>>>(
-      g, st, *ix, maps, (const B*)out, (const B*)dout, lse, delta, lse2, (B*)dq);
+      g, st, *ix, maps, lse, delta, lse2, (B*)dq);
   k_seq_dkdv<HD><<<(unsigned)(g.n_rows * g.Hk), NT, bk, s>>>(g, st, *ix, maps, delta, lse2, (B*)dk,
                                                              (B*)dv);
   count_launches(2);

@@ -50,16 +50,14 @@ template <int HD>
 struct Cfg {
   static constexpr int NSEG = HD > 64 ? 2 : 1;
   static constexpr uint32_t TILE = NSEG * SEG;
-  // key and value tiles in flight: two pairs (a fifth tile changed nothing) leave
-  // room for the output's staging
-  static constexpr int NST = HD > 64 ? 4 : 8;
+  // key and value tiles in flight: what 227 KB hold beside the two query tiles
+  static constexpr int NST = HD > 64 ? 5 : 8;
 };
 
 template <int HD>
 struct Smem {
   uint8_t q[2][Cfg<HD>::TILE];
   uint8_t kv[Cfg<HD>::NST][Cfg<HD>::TILE];  // ring: k_0, v_0, k_1, v_1, ...
-  uint4 stage[8][32 * 4];  // 32 rows x 32 channels of out per softmax warp
   uint64_t q_full[2];
   uint64_t full[Cfg<HD>::NST], empty[Cfg<HD>::NST];
   uint64_t s_full[2];     // S of the tile's next key tile computed
@@ -325,37 +323,29 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_after();
       const float inv = 1.f / l_run;
       const int64_t row = (int64_t)t.start + pos;
-      // the warp's first row, and its rows of the sequence
-      const int first = pos - lane;
-      __nv_bfloat16* dst = out + ((int64_t)t.start + first) * stride_out + (int64_t)h * g.d;
-      // Through shared memory, so that a store of the warp covers 8 rows of 64
-      // bytes (a row per lane, 16 bytes of 32 lines at a time, took 2,600 cycles).
-      // Piece c of row r stands at piece c ^ (r / 2 % 4): no bank conflicts.
-      uint4* stage = sm.stage[warp];
-#pragma unroll 1
-      for (int c0 = 0; c0 < HD; c0 += 32) {
+      __nv_bfloat16* dst = out + row * stride_out + (int64_t)h * g.d;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) {
         uint32_t o[32];
-        tmem_ld32(tO + c0, o);
+        tmem_ld32(tO + 32 * c, o);
         tmem_wait_ld();
+        if (pos < t.len) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[4];
+          for (int e = 0; e < 4; ++e) {
+            const int ch = 32 * c + 8 * e;
+            if (ch >= g.d) break;
+            const float2 f = make_float2(inv, inv);
+            uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * x]) * inv,
-                               __uint_as_float(o[8 * c + 2 * x + 1]) * inv);
-          stage[lane * 4 + (c ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int x = 0; x < 4; ++x) {
+              const float2 y = f2_mul(make_float2(__uint_as_float(o[8 * e + 2 * x]),
+                                                  __uint_as_float(o[8 * e + 2 * x + 1])),
+                                      f);
+              w[x] = pack_bf16x2(y.x, y.y);
+            }
+            *reinterpret_cast<uint4*>(dst + ch) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
-        __syncwarp();
-        const int ch = c0 + 8 * (lane & 3);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int rr = 8 * s + (lane >> 2);
-          if (first + rr < t.len && ch < g.d)
-            *reinterpret_cast<uint4*>(dst + rr * stride_out + ch) =
-                stage[rr * 4 + ((lane & 3) ^ ((rr >> 1) & 3))];
-        }
-        __syncwarp();
       }
       if (pos < t.len) lse[(int64_t)h * g.N + row] = (m_run + log2f(l_run)) * LN2;
     }
