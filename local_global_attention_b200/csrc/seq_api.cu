@@ -30,8 +30,8 @@ int make_geo(const pack3d_seq_params* p, SeqGeo* g) {
   // than n of them not empty
   const int64_t B = p->n_seqs, N = p->n_tokens;
   const int64_t pair = N / PAIR + B, rows = N / ROWS + B;
-  // launches have at most two blocks per (tile, head), and at most 2^31 - 1 blocks
-  if (2 * rows * p->Hq >= (int64_t)1 << 31) return PACK3D_ERR_ARG;
+  // launches have at most four blocks per (tile, head), and at most 2^31 - 1 blocks
+  if (4 * rows * p->Hq >= (int64_t)1 << 31) return PACK3D_ERR_ARG;
   g->n_pair = (int)pair;
   g->n_rows = (int)rows;
   return PACK3D_OK;

@@ -104,10 +104,10 @@ constexpr uint32_t QCOL_S = 0, QCOL_DP = 256, QCOL_ACC = 384;
 template <int HD>
 __global__ void __launch_bounds__(NT, 1)
     k_seq_dq(SeqGeo g, Strides st, pack3d_seq_index ix, const __grid_constant__ MapsB maps,
-             const float* __restrict__ lse, float* __restrict__ delta, float* __restrict__ lse2,
-             __nv_bfloat16* __restrict__ dq) {
+             const float* lse, float* delta, float* lse2, __nv_bfloat16* dq) {
   using C = Cfg<HD>;
   constexpr int NSEG = C::NSEG, NST = C::NST;
+  overlapped_start();
   const int h = blockIdx.x % g.Hq;
   const Tile t = load_tile_entry(ix.query, blockIdx.x / g.Hq);
   if (ix.err[0] || t.len == 0) return;
@@ -402,11 +402,11 @@ constexpr uint32_t KCOL_S = 0, KCOL_DP = 128, KCOL_DK = 256;
 template <int HD>
 __global__ void __launch_bounds__(NT, 1)
     k_seq_dkdv(SeqGeo g, Strides st, pack3d_seq_index ix, const __grid_constant__ MapsB maps,
-               const float* __restrict__ delta, const float* __restrict__ lse2,
-               __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+               const float* delta, const float* lse2, __nv_bfloat16* dk, __nv_bfloat16* dv) {
   using C = Cfg<HD>;
   constexpr int NSEG = C::NSEG, NST = C::NSTK;
   constexpr uint32_t KCOL_DV = KCOL_DK + HD;
+  overlapped_start();
   const int hk = blockIdx.x % g.Hk;
   const Tile t = load_tile_entry(ix.key, blockIdx.x / g.Hk);
   if (ix.err[0] || t.len == 0) return;
@@ -681,12 +681,12 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
           cudaSuccess)
     return PACK3D_ERR_CUDA;
   using B = __nv_bfloat16;
-  k_seq_dq<HD><<<(unsigned)(g.n_rows * g.Hq), NT, bq, s>>>(
-      g, st, *ix, maps, lse, delta, lse2, (B*)dq);
-  k_seq_dkdv<HD><<<(unsigned)(g.n_rows * g.Hk), NT, bk, s>>>(g, st, *ix, maps, delta, lse2, (B*)dk,
-                                                             (B*)dv);
   count_launches(2);
-  return cuda_status(cudaGetLastError());
+  const int rc = launch_overlapped(k_seq_dq<HD>, (unsigned)(g.n_rows * g.Hq), NT, bq, s, g, st, *ix,
+                                   maps, lse, delta, lse2, (B*)dq);
+  if (rc) return rc;
+  return launch_overlapped(k_seq_dkdv<HD>, (unsigned)(g.n_rows * g.Hk), NT, bk, s, g, st, *ix, maps,
+                           (const float*)delta, (const float*)lse2, (B*)dk, (B*)dv);
 }
 
 }  // namespace

@@ -92,10 +92,10 @@ __device__ __forceinline__ float exp_pack(const uint32_t* sv, float c2, float mn
 template <int HD>
 __global__ void __launch_bounds__(NT, 1)
     k_seq_forward_tc(SeqGeo g, int64_t stride_out, pack3d_seq_index ix,
-                     const __grid_constant__ Maps maps, __nv_bfloat16* __restrict__ out,
-                     float* __restrict__ lse) {
+                     const __grid_constant__ Maps maps, __nv_bfloat16* out, float* lse) {
   using C = Cfg<HD>;
   constexpr int NSEG = C::NSEG, NST = C::NST;
+  overlapped_start();
   const int h = blockIdx.x % g.Hq;
   const Tile t = load_tile_entry(ix.pair, blockIdx.x / g.Hq);
   if (ix.err[0] || t.len == 0) return;
@@ -380,10 +380,9 @@ int forward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, cons
   if (cudaFuncSetAttribute(k_seq_forward_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)bytes) != cudaSuccess)
     return PACK3D_ERR_CUDA;
-  k_seq_forward_tc<HD><<<(unsigned)(g.n_pair * g.Hq), NT, bytes, s>>>(
-      g, st.out, *ix, maps, (__nv_bfloat16*)out, lse);
   count_launches(1);
-  return cuda_status(cudaGetLastError());
+  return launch_overlapped(k_seq_forward_tc<HD>, (unsigned)(g.n_pair * g.Hq), NT, bytes, s, g, st.out,
+                           *ix, maps, (__nv_bfloat16*)out, lse);
 }
 
 }  // namespace

@@ -36,8 +36,10 @@ struct Tile {
   int start, len, off, pad;
 };
 
+// (A plain load: a read-only one may be moved ahead of the wait for the kernel
+// that wrote the list.)
 __device__ __forceinline__ Tile load_tile_entry(const int32_t* list, int i) {
-  const int4 x = __ldg(reinterpret_cast<const int4*>(list) + i);
+  const int4 x = reinterpret_cast<const int4*>(list)[i];
   return Tile{x.x, x.y, x.z, x.w};
 }
 

@@ -57,6 +57,34 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Launches that overlap the end of the kernel before them in the stream: the next
+// kernel's blocks may be placed once every block of this one has started and SMs
+// come free; the first thing they do is to wait until this one is complete and
+// its writes are visible, so an order of launches means what it always does.
+// What it saves is the launch latency between the kernels of one call (and of
+// calls in a row).  Global memory that an earlier kernel wrote is read through
+// plain pointers in these kernels (no __restrict__, no read-only loads): the
+// compiler may move read-only loads ahead of the wait.
+__device__ __forceinline__ void overlapped_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+inline int launch_overlapped(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem,
+                             cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
+}
+
 // A wait of a whole converged warp: true once the phase is complete, false when
 // some role of the CTA has given up or the poll limit is reached.  The vote keeps
 // the branch uniform: a wait on a completed phase takes 48 cycles, against 155
