@@ -51,30 +51,26 @@ struct Cfg {
   static constexpr int NST = HD > 64 ? 5 : 8, NSTK = HD > 64 ? 4 : 8;
 };
 
-// Word w of P or dS for 64 columns (two per word), packed from fp32.
+// 64 columns of P or dS (two bf16 per word) into tensor memory.
 __device__ __forceinline__ void store_half(uint32_t taddr, const uint32_t (&p)[32]) {
   tmem_st32(taddr, p);
   tmem_wait_st();
 }
 
-__device__ __forceinline__ void bar_elementwise() {
-  asm volatile("bar.sync 1, 256;" ::: "memory");
-}
-
-// Half `half` of the HD channels of a warp's 32 accumulator rows (HD / 2 is no
-// multiple of 32 at 96: that half overlaps the other's last 16 channels, and the
-// same values are stored twice).
+// The HD channels of a warp's 32 accumulator rows in pieces of 32, shared between
+// the two warps of the rows (three pieces at HD = 96: two and one).
 template <int HD>
 __device__ __forceinline__ void store_acc(uint32_t taddr, float f, __nv_bfloat16* dst,
                                           int64_t stride, int live, int half, int d, int lane) {
-  constexpr int N = (HD / 2 + 31) / 32;  // pieces of 32 channels
+  constexpr int N = HD / 32, FIRST = (N + 1) / 2;
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const int c0 = half ? HD - 32 * (c + 1) : 32 * c;
+  for (int c = 0; c < FIRST; ++c) {
+    const int piece = half * FIRST + c;
+    if (piece >= N) break;
     uint32_t o[32];
-    tmem_ld32(taddr + c0, o);
+    tmem_ld32(taddr + 32 * piece, o);
     tmem_wait_ld();
-    store_rows32(o, f, dst, stride, live, c0, d, lane);
+    store_rows32(o, f, dst, stride, live, 32 * piece, d, lane);
   }
 }
 
@@ -123,7 +119,7 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.do_full, 1);
     mbar_init(&sm.o_full, 1);
-    mbar_init(&sm.o_read, 8);  // one arrival per elementwise warp
+    mbar_init(&sm.o_read, 8);  // one arrival per elementwise warp (one key tile: their sums)
     for (int s = 0; s < NST; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
@@ -282,7 +278,8 @@ __global__ void __launch_bounds__(NT, 1)
       sm.part[half][r] = x;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.o_read);
-      bar_elementwise();
+      // (an mbarrier: its wait is bounded, that of a block barrier is not)
+      if (ok) ok = warp_wait(&sm.o_read, 0, abort_flag);
       dl = sm.part[0][r] + sm.part[1][r];
     }
     for (int j = 0; j < n && ok; ++j) {
@@ -328,7 +325,9 @@ __global__ void __launch_bounds__(NT, 1)
         // (one key tile leaves the ring's last slot unused)
         float2* sum = reinterpret_cast<float2*>(sm.kv[NST - 1]);
         sum[half * ROWS + r] = make_float2(a, b);
-        bar_elementwise();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_read);
+        if (!(ok = warp_wait(&sm.o_read, 0, abort_flag))) break;
         const float2 x = sum[r], y = sum[ROWS + r];
         dl = (x.x + y.x) / (x.y + y.y);
       }

@@ -14,10 +14,12 @@
 // running maximum and sum; the backward recomputes P from lse, once by query tile
 // (dq) and once by key tile, where S is formed transposed, so no sum crosses blocks.
 //
-// Bound by fp32 FMA and the shared-memory reads that feed it, and at the sizes of
-// the fp32 workloads by the longest row of tiles: 32-row blocks, four of which
-// fit an SM, took 0.17 ms for a training step of 2,000 tokens in four
-// sequences, 4 heads, d 48, against 0.41 ms with 64-row blocks of 256 threads.
+// Bound by fp32 FMA and the shared-memory reads that feed it (2.5 reads of a warp
+// per 12 FMA in the accumulation), and at the sizes of the fp32 workloads by the
+// latency of the longest row of tiles: a training step of 2,000 tokens in four
+// sequences, 4 heads, d 48, takes 0.29 ms (6.6 TFLOP/s).  64-row blocks of 256
+// threads without the double buffer took 0.41 ms, 32-row ones 0.37; 2 x 4 values
+// per thread and 256 threads 0.34 (more reads per FMA).
 #include <math.h>
 
 #include "seq_internal.cuh"
