@@ -510,10 +510,11 @@ def make_rotary_params(head_dim: int, rot_dim: int = None, layout: str = "half",
 class _Launch:
     """The device and stream of one packed-sequence call: every tensor on one
     device, which is current while the call launches; the given stream (of that
-    device) or the device's current one.  Buffers allocated here are recorded on
-    a given stream, so that the allocator does not hand them on early."""
+    device) or the device's current one.  With a given stream, buffers are
+    allocated on that stream (whose earlier work may still use the memory
+    otherwise) and recorded on the caller's."""
 
-    __slots__ = ("index", "given", "raw", "before")
+    __slots__ = ("index", "given", "raw", "before", "caller")
 
     def __init__(self, like, stream):
         self.index = index = like.get_device()
@@ -526,9 +527,13 @@ class _Launch:
                 stream = torch.cuda.ExternalStream(int(stream), device=index)
             if stream.device.index != index:
                 raise ValueError(f"the stream is on {stream.device}, the tensors on {like.device}")
-            self.given, self.raw = stream, stream.cuda_stream
+            self.caller = torch.cuda.current_stream(index)
+            self.given, self.raw = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
+        if self.given is not None:
+            self.given.__enter__()  # sets the device as well
+            return self
         now = torch._C._cuda_getDevice()
         self.before = None if now == self.index else now
         if self.before is not None:
@@ -536,7 +541,9 @@ class _Launch:
         return self
 
     def __exit__(self, *exc):
-        if self.before is not None:
+        if self.given is not None:
+            self.given.__exit__(*exc)
+        elif self.before is not None:
             torch.cuda.set_device(self.before)
 
     def rows(self, t, shape, dtype, what):
@@ -571,7 +578,7 @@ class _Launch:
 
     def kept(self, t):
         if self.given is not None:
-            t.record_stream(self.given)
+            t.record_stream(self.caller)
         return t
 
 

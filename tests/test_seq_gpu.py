@@ -249,6 +249,27 @@ def test_repeated_streams_and_graph(dtype):
     assert P.pack3d_seq_index_check(ix) == P.OK
 
 
+def test_memory_of_a_given_stream():
+    """Outputs of a call on a given stream never stand in memory that work queued
+    on the caller's stream still reads, although its owner is gone."""
+    n, H, d = 16384, 16, 128
+    q = torch.ones(n, H, d, dtype=torch.bfloat16, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    p = P.make_rotary_params(d)
+    side = torch.cuda.Stream()
+    total = torch.zeros(n, H, d, dtype=torch.bfloat16, device="cuda")
+    P.pack3d_rotary(p, pos, q, stream=side)
+    torch.cuda.synchronize()
+    x = torch.ones(n, H, d, dtype=torch.bfloat16, device="cuda")
+    for _ in range(200):
+        total.add_(x)
+    del x
+    outs = [P.pack3d_rotary(p, pos, q, stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert (total == 200).all()  # whole numbers up to 256 are exact in bf16
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
 def test_index_built_in_a_graph():
     """Lengths that change between replays of one captured graph."""
     p = P.make_seq_params(3, 400, 2, 1, 64, True, "bf16")
