@@ -681,11 +681,7 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
     return PACK3D_ERR_CUDA;
   constexpr size_t bq = sizeof(SmemQ<HD>) + 1024, bk = sizeof(SmemK<HD>) + 1024;
   static_assert(bq <= 232448 && bk <= 232448, "shared memory of a CTA");
-  if (cudaFuncSetAttribute(k_seq_dq<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bq) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(k_seq_dkdv<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bk) !=
-          cudaSuccess)
-    return PACK3D_ERR_CUDA;
+  if (!allow_smem<k_seq_dq<HD>>(bq) || !allow_smem<k_seq_dkdv<HD>>(bk)) return PACK3D_ERR_CUDA;
   using B = __nv_bfloat16;
   count_launches(2);
   const int rc = launch_overlapped(k_seq_dq<HD>, (unsigned)(g.n_rows * g.Hq), NT, bq, s, g, st, *ix,

@@ -385,9 +385,7 @@ int forward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, cons
     return PACK3D_ERR_CUDA;
   constexpr size_t bytes = sizeof(Smem<HD>) + 1024;  // + alignment slack
   static_assert(bytes <= 232448, "shared memory of a CTA");
-  if (cudaFuncSetAttribute(k_seq_forward_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)bytes) != cudaSuccess)
-    return PACK3D_ERR_CUDA;
+  if (!allow_smem<k_seq_forward_tc<HD>>(bytes)) return PACK3D_ERR_CUDA;
   count_launches(1);
   return launch_overlapped(k_seq_forward_tc<HD>, (unsigned)(g.n_pair * g.Hq), NT, bytes, s, g, st.out,
                            *ix, maps, (__nv_bfloat16*)out, lse);

@@ -3,6 +3,8 @@
 // positions.
 #pragma once
 
+#include <atomic>
+
 #include "pack3d_internal.cuh"
 
 namespace p3d {
@@ -41,6 +43,22 @@ struct Tile {
 __device__ __forceinline__ Tile load_tile_entry(const int32_t* list, int i) {
   const int4 x = reinterpret_cast<const int4*>(list)[i];
   return Tile{x.x, x.y, x.z, x.w};
+}
+
+// Let KERNEL use `bytes` of dynamic shared memory on the current device (asked for
+// once per device: the runtime call costs as much host time as a tensor map).
+template <auto KERNEL>
+inline bool allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) !=
+      cudaSuccess)
+    return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
 }
 
 int make_geo(const pack3d_seq_params* p, SeqGeo* g);

@@ -15,11 +15,12 @@
 // (dq) and once by key tile, where S is formed transposed, so no sum crosses blocks.
 //
 // Bound by fp32 FMA and the shared-memory reads that feed it (2.5 reads of a warp
-// per 12 FMA in the accumulation), and at the sizes of the fp32 workloads by the
-// latency of the longest row of tiles: a training step of 2,000 tokens in four
-// sequences, 4 heads, d 48, takes 0.29 ms (6.6 TFLOP/s).  64-row blocks of 256
-// threads without the double buffer took 0.41 ms, 32-row ones 0.37; 2 x 4 values
-// per thread and 256 threads 0.34 (more reads per FMA).
+// per 12 FMA in the accumulation; pairs of FMA in one instruction), and at the
+// sizes of the fp32 workloads by the latency of the longest row of tiles: a
+// training step of 2,000 tokens in four sequences, 4 heads, d 48, takes 0.27 ms
+// (7.2 TFLOP/s; 0.29 with single FMA).  64-row blocks of 256 threads without the
+// double buffer took 0.41 ms, 32-row ones 0.37; 2 x 4 values per thread and 256
+// threads 0.34 (more reads per FMA).
 #include <math.h>
 
 #include "seq_internal.cuh"
@@ -69,11 +70,12 @@ struct Stream {
 template <int HD>
 __device__ __forceinline__ void dot_tile(float (&s)[4][4], const float* a, const float* b, int tx,
                                          int ty) {
+  float2 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
+    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
+#pragma unroll 6
   for (int c = 0; c < HD; c += 4) {
     float4 x[4], y[4];
 #pragma unroll
@@ -86,12 +88,14 @@ __device__ __forceinline__ void dot_tile(float (&s)[4][4], const float* a, const
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
-        s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
-        s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
-        s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+        acc[i][j] = tc::f2_fma(make_float2(x[i].x, x[i].y), make_float2(y[j].x, y[j].y), acc[i][j]);
+        acc[i][j] = tc::f2_fma(make_float2(x[i].z, x[i].w), make_float2(y[j].z, y[j].w), acc[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
 }
 
 // Four rows of an accumulator: channels 2 tx + 32 j + {0, 1}, and 32 N2 + tx where
@@ -120,7 +124,7 @@ struct Acc {
   }
   // row i += sum_k p[4 ty + i][k] b_row(k)
   __device__ __forceinline__ void add(const float* p, const float* b, int tx, int ty) {
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < TC; k += 4) {
       float4 w[4];
 #pragma unroll
@@ -137,8 +141,7 @@ struct Acc {
           const float2 y = *reinterpret_cast<const float2*>(row + 2 * tx + 32 * j);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            two[i][j].x = fmaf(f(i), y.x, two[i][j].x);
-            two[i][j].y = fmaf(f(i), y.y, two[i][j].y);
+            two[i][j] = tc::f2_fma(make_float2(f(i), f(i)), y, two[i][j]);
           }
         }
         if (N1) {
@@ -423,17 +426,11 @@ constexpr size_t smem_bytes(int own, int weights) {
   return sizeof(float) * ((size_t)(own * TR + 4 * TC) * (HD + PAD) + (size_t)weights * TR * PS);
 }
 
-template <typename K>
-bool allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-         cudaSuccess;
-}
-
 template <int HD>
 int forward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, const float* q,
             const float* k, const float* v, float* out, float* lse, cudaStream_t s) {
   constexpr size_t bytes = smem_bytes<HD>(1, 1);
-  if (!allow_smem(k_seq_forward_simt<HD>, bytes)) return PACK3D_ERR_CUDA;
+  if (!allow_smem<k_seq_forward_simt<HD>>(bytes)) return PACK3D_ERR_CUDA;
   k_seq_forward_simt<HD>
       <<<dim3(SUB * g.n_rows, g.Hq), NT, bytes, s>>>(g, st, *ix, q, k, v, out, lse);
   count_launches(1);
@@ -445,7 +442,7 @@ int backward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, con
              const float* k, const float* v, const float* out, const float* lse, const float* dout,
              float* dq, float* dk, float* dv, float* delta, cudaStream_t s) {
   constexpr size_t b_dq = smem_bytes<HD>(2, 1), b_kv = smem_bytes<HD>(2, 2);
-  if (!allow_smem(k_seq_dq_simt<HD>, b_dq) || !allow_smem(k_seq_dkdv_simt<HD>, b_kv))
+  if (!allow_smem<k_seq_dq_simt<HD>>(b_dq) || !allow_smem<k_seq_dkdv_simt<HD>>(b_kv))
     return PACK3D_ERR_CUDA;
   const int64_t warps = (int64_t)g.N * g.Hq;
   k_seq_delta<<<(unsigned)((warps + NT / 32 - 1) / (NT / 32)), NT, 0, s>>>(g, st, *ix, out, dout,
