@@ -35,7 +35,7 @@
 // to 1.57 GHz); 16,384 tokens not causal, 8 heads, d 96, 0.88-0.98 ms.  Bound by the
 // chain S - softmax - P v of a tile (3,230 cycles a step of both tiles at d 128,
 // 2,960 at d 96, against 2,140 and 1,610 of tensor work) and, in long runs, by
-// power.  Short sequences pay about 8,000 cycles per CTA for set-up, first loads
+// power.  Short sequences pay about 7,000 cycles per CTA for set-up, first loads
 // and output.
 #include <cuda.h>
 #include <math.h>
@@ -79,6 +79,7 @@ struct Smem {
 
 struct Maps {
   CUtensorMap q, k, v;
+  CUtensorMap out;  // boxes of 32 rows
 };
 
 // P = 2^(S c - m) of 32 keys into 16 words; returns the sum.
@@ -142,6 +143,7 @@ __global__ void __launch_bounds__(NT, 1)
     tma_prefetch_map(&maps.q);
     tma_prefetch_map(&maps.k);
     tma_prefetch_map(&maps.v);
+    tma_prefetch_map(&maps.out);
   }
   if (warp == MMA_WARP) {
     tmem_alloc(&sm.tmem_base, TMEM_COLS);
@@ -298,7 +300,11 @@ __global__ void __launch_bounds__(NT, 1)
         m_run = top;
       }
       if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll
+        // (Unrolled at 64 and 128; at 96 the compiler then spills 52 bytes in the row
+        // loop: 40.9 against 38.7 us for a ragged batch.  Rolled at 128: 3.89
+        // against 3.72 ms for 32,768 tokens.)
+        constexpr int UNROLL = HD == 96 ? 1 : HD / 32;
+#pragma unroll UNROLL
         for (int c = 0; c < HD / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * c, o);
@@ -331,31 +337,52 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_after();
       const float inv = 1.f / l_run;
       const int64_t row = (int64_t)t.start + pos;
-      __nv_bfloat16* dst = out + row * stride_out + (int64_t)h * g.d;
-#pragma unroll
-      for (int c = 0; c < HD / 32; ++c) {
+      if (pos < t.len) lse[(int64_t)h * g.N + row] = (m_run + log2f(l_run)) * LN2;
+      // Out through the query tile's shared memory (every product that read it is
+      // done), in the layout the query came in, by TMA where the warp's 32 rows are
+      // all the sequence's, else by pieces of 128 bytes.  Straight from registers, a
+      // row per lane, the stores took 2,600 cycles at 128 channels (shortest training
+      // step at d 96: forward 9.9 against 8.2 us).
+      uint8_t* tile = sm.q[i];
+#pragma unroll 1
+      for (int c0 = 0; c0 < HD; c0 += 32) {
         uint32_t o[32];
-        tmem_ld32(tO + 32 * c, o);
+        tmem_ld32(tO + c0, o);
         tmem_wait_ld();
-        if (pos < t.len) {
+        uint8_t* to = tile + (c0 >> 6) * SEG + r * 128;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int ch = 32 * c + 8 * e;
-            if (ch >= g.d) break;
-            const float2 f = make_float2(inv, inv);
-            uint32_t w[4];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 y = f2_mul(make_float2(__uint_as_float(o[8 * e + 2 * x]),
-                                                  __uint_as_float(o[8 * e + 2 * x + 1])),
-                                      f);
-              w[x] = pack_bf16x2(y.x, y.y);
-            }
-            *reinterpret_cast<uint4*>(dst + ch) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int x = 0; x < 4; ++x)
+            w[x] = pack_bf16x2(__uint_as_float(o[8 * c + 2 * x]) * inv,
+                               __uint_as_float(o[8 * c + 2 * x + 1]) * inv);
+          *reinterpret_cast<uint4*>(to + ((((c0 & 32) >> 3) + c) ^ (r & 7)) * 16) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (pos < t.len) lse[(int64_t)h * g.N + row] = (m_run + log2f(l_run)) * LN2;
+      const int first = pos - lane, live = t.len - first;  // the warp's first row, its rows
+      tile += (r - lane) * 128;
+      if (live >= 32) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+          for (int s = 0; s < NSEG; ++s)
+            tma_store_3d(&maps.out, tile + s * SEG, 64 * s, h, t.start + first);
+          tma_store_wait();
+        }
+      } else {
+        __syncwarp();
+        __nv_bfloat16* dst = out + (row - lane) * stride_out + (int64_t)h * g.d;
+        for (int x = lane; x < live * 8 * NSEG; x += 32) {
+          const int rr = x / (8 * NSEG), c = x % (8 * NSEG);
+          if (8 * c < g.d)
+            *reinterpret_cast<uint4*>(dst + rr * stride_out + 8 * c) =
+                *reinterpret_cast<const uint4*>(tile + (c >> 3) * SEG + rr * 128 +
+                                                (((c & 7) ^ (rr & 7)) << 4));
+        }
+      }
     }
   }
 
@@ -381,7 +408,8 @@ int forward(const SeqGeo& g, const Strides& st, const pack3d_seq_index* ix, cons
   Maps maps;
   if (!encode_rows(&maps.q, q, g.d, g.Hq, g.N, st.q, ROWS) ||
       !encode_rows(&maps.k, k, g.d, g.Hk, g.N, st.k, ROWS) ||
-      !encode_rows(&maps.v, v, g.d, g.Hk, g.N, st.v, ROWS))
+      !encode_rows(&maps.v, v, g.d, g.Hk, g.N, st.v, ROWS) ||
+      !encode_rows(&maps.out, out, g.d, g.Hq, g.N, st.out, 32))
     return PACK3D_ERR_CUDA;
   constexpr size_t bytes = sizeof(Smem<HD>) + 1024;  // + alignment slack
   static_assert(bytes <= 232448, "shared memory of a CTA");

@@ -121,6 +121,22 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane) {
   __syncwarp();
 }
 
+// One box of a 3-D tensor map from shared memory to global memory (what lies
+// outside the tensor is not written), and the wait until this thread's boxes are
+// written.
+__device__ __forceinline__ void tma_store_3d(const void* map, const void* src, int c0, int c1,
+                                             int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(src))
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // 32 channels [c0, c0 + 32) of a warp's 32 accumulator rows (lane = row), scaled
 // and rounded to bf16, into rows `stride` elements apart from dst on: rows below
 // `live`, channels below d.  Four lanes first exchange their 16-byte pieces, so
