@@ -438,6 +438,7 @@ typedef struct {
   int32_t* key;
   int32_t* err;
   int32_t n_pair, n_rows; /* entries of pair; of query and of key (some unused) */
+  int32_t n_seqs, n_tokens; /* of the params it was carved for; every call checks them */
 } pack3d_seq_index;
 
 /* Bytes of device memory an index needs (0 if the params are invalid).

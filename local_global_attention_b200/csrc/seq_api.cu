@@ -81,7 +81,11 @@ Layout index_layout(const SeqGeo& g) {
 int check_index(const SeqGeo& g, const pack3d_seq_index* ix) {
   if (!ix || !ix->pos || !ix->seq || !ix->pair || !ix->query || !ix->key || !ix->err)
     return PACK3D_ERR_ARG;
-  return ix->n_pair == g.n_pair && ix->n_rows == g.n_rows ? PACK3D_OK : PACK3D_ERR_ARG;
+  // the buffer was sized for these
+  return ix->n_pair == g.n_pair && ix->n_rows == g.n_rows && ix->n_seqs == g.B &&
+                 ix->n_tokens == g.N
+             ? PACK3D_OK
+             : PACK3D_ERR_ARG;
 }
 
 // Tensors start on 16-byte boundaries (the tensor maps and the vector accesses).
@@ -127,6 +131,8 @@ int pack3d_seq_index_init(const pack3d_seq_params* p, void* buffer, size_t bytes
   out->err = (int32_t*)(base + L.err);
   out->n_pair = g.n_pair;
   out->n_rows = g.n_rows;
+  out->n_seqs = g.B;
+  out->n_tokens = g.N;
   return PACK3D_OK;
 }
 

@@ -63,7 +63,7 @@ class SeqStrides(ctypes.Structure):
 
 class SeqIndexStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("pos", "seq", "pair", "query", "key", "err")] + [
-        ("n_pair", ctypes.c_int32), ("n_rows", ctypes.c_int32)]
+        (n, ctypes.c_int32) for n in ("n_pair", "n_rows", "n_seqs", "n_tokens")]
 
 
 class RotaryParams(ctypes.Structure):
@@ -591,7 +591,8 @@ class SeqIndex:
         if nbytes == 0:
             raise Pack3dError(ERR_ARG, "pack3d_seq_index_bytes")
         self.params = params
-        self.buffer = torch.empty(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
+        # zeros: calls with an index that was never built find no tile
+        self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         self.device = self.buffer.get_device()
         self.struct = SeqIndexStruct()
         base = self.buffer.data_ptr()

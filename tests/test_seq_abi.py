@@ -83,6 +83,21 @@ def test_index_sizes(lib):
     assert lib.pack3d_seq_index_check(None, None) == P.ERR_ARG
 
 
+@pytest.mark.parametrize("built,used", [(dict(n_tokens=896), dict(n_tokens=1023)),
+                                        (dict(n_tokens=1023), dict(n_tokens=896)),
+                                        (dict(n_seqs=4, n_tokens=128), dict(n_seqs=5, n_tokens=0))])
+def test_index_of_other_params(lib, built, used):
+    """An index whose lists have the same lengths but whose rows were sized for
+    other params (896 rows end where 1,023 rows would still write)."""
+    ix, n0 = index(lib, params(**built)), P.pack3d_kernel_launches()
+    p = params(**used)
+    other = index(lib, p)
+    assert (ix.n_rows == other.n_rows) and ix.n_tokens != other.n_tokens
+    assert lib.pack3d_seq_build_index(p, FAKE, ix, None) == P.ERR_ARG
+    assert forward(lib, p, ix) == P.ERR_ARG and backward(lib, p, ix) == P.ERR_ARG
+    assert P.pack3d_kernel_launches() == n0
+
+
 @pytest.mark.parametrize("what", ["q", "k", "v", "out", "lse"])
 def test_forward_pointers(lib, what):
     p = params()

@@ -308,6 +308,20 @@ def test_binding_refusals():
         P.pack3d_seq_build_index(p, torch.zeros(4, dtype=torch.int32, device="cuda"))
 
 
+def test_index_that_was_never_built():
+    p = P.make_seq_params(2, 300, 2, 1, 64, True, "bf16")
+    ix = P.SeqIndex(p)
+    q, k, v, dout = S.make([300], 2, 1, 64, "bf16")
+    kept = [torch.full_like(q, 7) for _ in range(2)]
+    lse = torch.zeros(2, 300, device="cuda")
+    P.pack3d_seq_forward(p, ix, q, k, v, kept[0], lse)
+    P.pack3d_seq_backward(p, ix, q, k, v, q, lse, dout, dq=kept[1])
+    assert all((x == 7).all() for x in kept) and not lse.any()
+    with pytest.raises(P.Pack3dError):  # an index of other params
+        P.pack3d_seq_forward(P.make_seq_params(2, 301, 2, 1, 64), ix, *S.make([301], 2, 1, 64,
+                                                                             "bf16")[:3])
+
+
 def test_empty_pack():
     p, ix = built([0, 0], 2, 1, 64, True, "bf16")
     q, k, v, dout = S.make([0], 2, 1, 64, "bf16")
