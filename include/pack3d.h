@@ -379,7 +379,8 @@ PACK3D_API const char* pack3d_strerror(int status);
  *
  * Sequence s holds the rows [cu[s], cu[s + 1]) of the packed tensors, cu the
  * prefix sums of the lengths (cu[0] = 0; a length may be 0).  Rows behind
- * cu[n_seqs] belong to no sequence: they are read nowhere and written nowhere.
+ * cu[n_seqs] belong to no sequence: nothing of them enters a result, and the
+ * outputs' are left as they were (zeros with PACK3D_ZERO_UNUSED_ROWS).
  * Query head h uses key/value head h / (Hq / Hk).  With P the softmax over the
  * row's own sequence (its tokens up to and including itself when causal):
  *
@@ -400,6 +401,12 @@ PACK3D_API const char* pack3d_strerror(int status);
  * or query of a token may also reach rows of up to 256 tokens before it (a
  * masked weight of zero times that value). */
 
+/* Or'ed into the dtype of a packed-sequence or rotary call's params: the call
+ * writes zeros to the outputs' rows that belong to no sequence (rotary: whose
+ * position is negative), for outputs in memory that nobody has written yet.  An
+ * index that holds an error has no rows: nothing is written. */
+enum { PACK3D_ZERO_UNUSED_ROWS = 0x100 };
+
 /* head_dim a multiple of 8, 8 .. 128; Hq a multiple of Hk; 1 <= n_seqs,
  * 0 <= n_tokens <= 2^30; Hq <= 65535. */
 typedef struct {
@@ -408,7 +415,7 @@ typedef struct {
   int32_t Hq, Hk, head_dim;
   int32_t causal;   /* nonzero: token i sees the tokens of its sequence up to itself */
   float scale;      /* softmax scale; <= 0 selects 1 / sqrt(head_dim) */
-  int32_t dtype;    /* PACK3D_BF16 or PACK3D_FP32 */
+  int32_t dtype;    /* PACK3D_BF16 or PACK3D_FP32 (| PACK3D_ZERO_UNUSED_ROWS) */
 } pack3d_seq_params;
 
 /* Elements between two tokens of each tensor; 0 (or a NULL struct) for tensors
@@ -428,7 +435,8 @@ typedef struct {
  *                           costliest tiles first: 256-row query tiles,
  *                           128-row query tiles, 128-row key tiles
  *   err   int32 [2]         [0]: 0 or a bit set of 1 = bad lengths, 4 = a kernel
- *                           gave up a bounded device-side wait
+ *                           gave up a bounded device-side wait; [1]: rows that
+ *                           the sequences hold (cu[n_seqs]; 0 for bad lengths)
  */
 typedef struct {
   int32_t* pos;
@@ -506,7 +514,7 @@ enum {
 typedef struct {
   int32_t n_tokens, Hq, Hk, head_dim; /* head_dim a multiple of 8, at most 256; Hk may be 0 */
   int32_t rot_dim;                    /* even, 2 .. head_dim */
-  int32_t layout, dtype;
+  int32_t layout, dtype;              /* dtype may hold PACK3D_ZERO_UNUSED_ROWS */
   float base;                         /* > 0 (RAMP: > 1) */
   int32_t scaling;
   float factor;                       /* >= 1 (not read by NONE) */
@@ -518,7 +526,7 @@ typedef struct {
 
 /* q_out = R(positions) q, k_out = R(positions) k (k, k_out ignored when Hk is
  * 0), with any position >= 0 at full precision; rows whose position is
- * negative are left as they were.  positions: int32 [n_tokens], device.
+ * negative are left as they were (or zeroed, see above).  positions: int32 [n_tokens], device.
  * q_out may be q and k_out may be k (same stride); no other overlap.  No
  * workspace, no index: one token of each running sequence is the same call
  * with n_tokens rows. */

@@ -15,7 +15,8 @@ int make_geo(const pack3d_seq_params* p, SeqGeo* g) {
   if (p->Hq < 1 || p->Hk < 1 || p->Hq > 65535 || p->Hq % p->Hk || p->head_dim < 1)
     return PACK3D_ERR_ARG;
   if (!isfinite(p->scale)) return PACK3D_ERR_ARG;
-  if (p->dtype != PACK3D_BF16 && p->dtype != PACK3D_FP32) return PACK3D_ERR_ARG;
+  const int dtype = p->dtype & ~PACK3D_ZERO_UNUSED_ROWS;
+  if (dtype != PACK3D_BF16 && dtype != PACK3D_FP32) return PACK3D_ERR_ARG;
   if (p->head_dim % 8 || p->head_dim > MAX_DIM) return PACK3D_ERR_UNSUPPORTED;
   g->B = p->n_seqs;
   g->N = p->n_tokens;
@@ -25,7 +26,8 @@ int make_geo(const pack3d_seq_params* p, SeqGeo* g) {
   g->d = p->head_dim;
   g->causal = p->causal != 0;
   g->tau = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->head_dim);
-  g->dtype = p->dtype;
+  g->dtype = dtype;
+  g->zero = dtype != p->dtype;
   // a sequence of n rows has at most floor(n / T) + 1 tiles of T rows, no more
   // than n of them not empty
   const int64_t B = p->n_seqs, N = p->n_tokens;

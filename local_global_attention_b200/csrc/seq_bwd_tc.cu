@@ -113,7 +113,12 @@ __global__ void __launch_bounds__(NT, 1)
   overlapped_start();
   const int h = blockIdx.x % g.Hq;
   const Tile t = load_tile_entry(ix.query, blockIdx.x / g.Hq);
-  if (ix.err[0] || t.len == 0) return;
+  const int64_t window = (int64_t)(blockIdx.x / g.Hq) * ROWS;
+  const State now = load_state(ix);
+  if (now.err) return;
+  if (unused_rows(g, now.rows, window, ROWS))
+    zero_unused(g, now.rows, window, ROWS, dq + (int64_t)h * g.d, st.dq);
+  if (t.len == 0) return;
   extern __shared__ uint8_t smem_raw[];
   SmemQ<HD>& sm = *reinterpret_cast<SmemQ<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~(uintptr_t)1023);
@@ -415,7 +420,14 @@ __global__ void __launch_bounds__(NT, 1)
   overlapped_start();
   const int hk = blockIdx.x % g.Hk;
   const Tile t = load_tile_entry(ix.key, blockIdx.x / g.Hk);
-  if (ix.err[0] || t.len == 0) return;
+  const int64_t window = (int64_t)(blockIdx.x / g.Hk) * ROWS;
+  const State now = load_state(ix);
+  if (now.err) return;
+  if (unused_rows(g, now.rows, window, ROWS)) {
+    zero_unused(g, now.rows, window, ROWS, dk + (int64_t)hk * g.d, st.dk);
+    zero_unused(g, now.rows, window, ROWS, dv + (int64_t)hk * g.d, st.dv);
+  }
+  if (t.len == 0) return;
   extern __shared__ uint8_t smem_raw[];
   SmemK<HD>& sm = *reinterpret_cast<SmemK<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~(uintptr_t)1023);

@@ -107,7 +107,15 @@ __global__ void __launch_bounds__(NT, 1)
   overlapped_start();
   const int h = blockIdx.x % g.Hq;
   const Tile t = load_tile_entry(ix.pair, blockIdx.x / g.Hq);
-  if (ix.err[0] || t.len == 0) return;
+  const int64_t window = (int64_t)(blockIdx.x / g.Hq) * PAIR;
+  const State now = load_state(ix);
+  if (now.err) return;
+  if (unused_rows(g, now.rows, window, PAIR)) {
+    zero_unused(g, now.rows, window, PAIR, out + (int64_t)h * g.d, stride_out);
+    const int64_t row = window + threadIdx.x;
+    if (threadIdx.x < PAIR && row >= now.rows && row < g.N) lse[(int64_t)h * g.N + row] = 0.f;
+  }
+  if (t.len == 0) return;
   extern __shared__ uint8_t smem_raw[];
   Smem<HD>& sm = *reinterpret_cast<Smem<HD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~(uintptr_t)1023);

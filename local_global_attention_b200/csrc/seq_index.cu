@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(NT)
     for (int i = tid; i < slots; i += NT) out[i] = Tile{0, 0, 0, 0};
     return;
   }
+  if (list == 0 && tid == 0) ix.err[1] = cu_in[g.B];
   const int T = list == LIST_PAIR ? PAIR : ROWS;
   int shift = 0;  // cost classes of 2^shift tiles of 128 columns
   while (((g.N / ROWS + 1) >> shift) >= CLASSES) ++shift;

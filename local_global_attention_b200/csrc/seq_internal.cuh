@@ -23,6 +23,7 @@ struct SeqGeo {
   int causal;
   float tau;               // softmax scale
   int dtype;
+  int zero;                // outputs' rows of no sequence become zero
   int n_pair, n_rows;      // entries of the 256-row and of the 128-row tile lists
 };
 
@@ -43,6 +44,34 @@ struct Tile {
 __device__ __forceinline__ Tile load_tile_entry(const int32_t* list, int i) {
   const int4 x = reinterpret_cast<const int4*>(list)[i];
   return Tile{x.x, x.y, x.z, x.w};
+}
+
+// The index's error word and the rows that its sequences hold (cu[n_seqs]).
+struct State {
+  int err, rows;
+};
+__device__ __forceinline__ State load_state(const pack3d_seq_index& ix) {
+  const int2 x = *reinterpret_cast<const int2*>(ix.err);
+  return State{x.x, x.y};
+}
+
+// Zeros into those of the rows [first, first + n) of one head that belong to no
+// sequence (`rows` of them do), by one block.  Block b of a launch over the tile
+// lists takes the rows [b T, b T + T), whatever tile it has: a list has at least
+// ceil(N / T) entries.
+__device__ __forceinline__ bool unused_rows(const SeqGeo& g, int rows, int64_t first, int n) {
+  // (unlikely: the zeroing then stands behind the kernel's way through its code)
+  return __builtin_expect(g.zero && first < g.N && rows < min((int64_t)g.N, first + n), 0);
+}
+template <typename T>
+__device__ __forceinline__ void zero_unused(const SeqGeo& g, int rows, int64_t first, int n,
+                                            T* head, int64_t stride) {
+  constexpr int E = 16 / sizeof(T);
+  const int pieces = g.d / E;
+  const int64_t from = max((int64_t)rows, first), end = min((int64_t)g.N, first + n);
+  for (int i = threadIdx.x; i < (int)(end - from) * pieces; i += blockDim.x)
+    *reinterpret_cast<uint4*>(head + (from + i / pieces) * stride + i % pieces * E) =
+        make_uint4(0, 0, 0, 0);
 }
 
 // Let KERNEL use `bytes` of dynamic shared memory on the current device (asked for

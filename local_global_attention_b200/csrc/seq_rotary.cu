@@ -42,6 +42,7 @@ constexpr int CS_ENTRIES = 2048; // (cos, sin) pairs of a group of rows in share
 struct RotArgs {
   uint64_t freq[MAX_PAIRS];  // theta_j / (2 pi), 64-bit binary fraction
   float amp, sense;          // sense -1: the transpose
+  int zero;                  // rows of a negative position become zero
   int half, r, d, n;         // pairs, rotated channels, head dim, rows
   int Hq, Hk;
   int units;                 // threads of a head: VEC pairs or channels turned, then copied
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(NT)
   const T* src = is_k ? k + (int64_t)(h - a.Hq) * a.d + ch : q + (int64_t)h * a.d + ch;
   T* dst = is_k ? ko + (int64_t)(h - a.Hq) * a.d + ch : qo + (int64_t)h * a.d + ch;
   // in place, the copied channels are there already
-  const bool mine = col < a.cols && (turned || src != dst);
+  const bool mine = col < a.cols && (turned || src != dst || a.zero);
   const int entry = HALF ? ch : ch / 2;
   const int rows = a.slots * ROWS_T;  // of a group
   int side = 0;
@@ -140,9 +141,15 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
     for (int i = 0; i < ROWS_T; ++i) {
       const int r = slot + i * a.slots;
-      // a negative position: behind the last sequence, left as it was
-      if (!mine || r >= live || pos[row0 + r] < 0) continue;
+      if (!mine || r >= live) continue;
       T* p = dst + (row0 + r) * so;
+      if (pos[row0 + r] < 0) {  // behind the last sequence
+        if (a.zero) {
+          store(p, V{});
+          if (HALF && turned) store(p + a.half, V{});
+        }
+        continue;
+      }
       if (turned) {
         const float2* c = cs + r * a.half + entry;
 #pragma unroll
@@ -263,7 +270,8 @@ int check_params(const pack3d_rotary_params* p) {
   if (p->n_tokens > (1 << 30)) return PACK3D_ERR_ARG;
   if (p->head_dim < 1 || p->rot_dim < 2 || (p->rot_dim & 1) || p->rot_dim > p->head_dim)
     return PACK3D_ERR_ARG;
-  if (p->dtype != PACK3D_BF16 && p->dtype != PACK3D_FP32) return PACK3D_ERR_ARG;
+  const int dtype = p->dtype & ~PACK3D_ZERO_UNUSED_ROWS;
+  if (dtype != PACK3D_BF16 && dtype != PACK3D_FP32) return PACK3D_ERR_ARG;
   if (p->layout != PACK3D_ROTARY_HALF && p->layout != PACK3D_ROTARY_INTERLEAVED)
     return PACK3D_ERR_ARG;
   if (!(p->base > 0.f) || !isfinite(p->base)) return PACK3D_ERR_ARG;
@@ -306,6 +314,7 @@ int rotary(const pack3d_rotary_params* p, const int32_t* pos, const void* q, con
   }
   a.amp = p->amplitude > 0.f ? p->amplitude : (float)amp;
   a.sense = sense;
+  a.zero = (p->dtype & PACK3D_ZERO_UNUSED_ROWS) != 0;
   a.r = p->rot_dim;
   a.d = p->head_dim;
   a.n = p->n_tokens;
@@ -327,7 +336,7 @@ int rotary(const pack3d_rotary_params* p, const int32_t* pos, const void* q, con
     return PACK3D_ERR_ARG;
   // In place means the same rows: another pitch would write rows not read yet.
   if ((q == qo && a.sq != a.soq) || (p->Hk && k == ko && a.sk != a.sok)) return PACK3D_ERR_ARG;
-  return p->dtype == PACK3D_BF16
+  return (p->dtype & ~PACK3D_ZERO_UNUSED_ROWS) == PACK3D_BF16
              ? launch_type<__nv_bfloat16>(a, p->layout, pos, q, k, qo, ko, s)
              : launch_type<float>(a, p->layout, pos, q, k, qo, ko, s);
 }

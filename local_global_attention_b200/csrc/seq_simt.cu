@@ -184,7 +184,16 @@ __global__ void __launch_bounds__(NT)
                        float* __restrict__ out, float* __restrict__ lse) {
   Tile t;
   int off, rows;
-  if (ix.err[0] || !own_rows(ix.query, t, off, rows)) return;
+  const State now = load_state(ix);
+  if (now.err) return;
+  const int64_t window = (int64_t)blockIdx.x * TR;
+  if (unused_rows(g, now.rows, window, TR)) {
+    zero_unused(g, now.rows, window, TR, out + (int64_t)blockIdx.y * g.d, st.out);
+    const int64_t row = window + threadIdx.x;
+    if (threadIdx.x < TR && row >= now.rows && row < g.N)
+      lse[(int64_t)blockIdx.y * g.N + row] = 0.f;
+  }
+  if (!own_rows(ix.query, t, off, rows)) return;
   extern __shared__ float sm[];
   float* sq = sm;
   const Stream<HD> kv = {sq + TR * (HD + PAD)};
@@ -284,7 +293,12 @@ __global__ void __launch_bounds__(NT)
                   const float* __restrict__ dout, float* __restrict__ dq) {
   Tile t;
   int off, rows;
-  if (ix.err[0] || !own_rows(ix.query, t, off, rows)) return;
+  const State now = load_state(ix);
+  if (now.err) return;
+  const int64_t window = (int64_t)blockIdx.x * TR;
+  if (unused_rows(g, now.rows, window, TR))
+    zero_unused(g, now.rows, window, TR, dq + (int64_t)blockIdx.y * g.d, st.dq);
+  if (!own_rows(ix.query, t, off, rows)) return;
   extern __shared__ float sm[];
   float *sq = sm, *sdo = sq + TR * (HD + PAD);
   const Stream<HD> kv = {sdo + TR * (HD + PAD)};
@@ -350,7 +364,14 @@ __global__ void __launch_bounds__(NT)
                     float* __restrict__ dv) {
   Tile t;
   int off, rows;
-  if (ix.err[0] || !own_rows(ix.key, t, off, rows)) return;
+  const State now = load_state(ix);
+  if (now.err) return;
+  const int64_t window = (int64_t)blockIdx.x * TR;
+  if (unused_rows(g, now.rows, window, TR)) {
+    zero_unused(g, now.rows, window, TR, dk + (int64_t)blockIdx.y * g.d, st.dk);
+    zero_unused(g, now.rows, window, TR, dv + (int64_t)blockIdx.y * g.d, st.dv);
+  }
+  if (!own_rows(ix.key, t, off, rows)) return;
   extern __shared__ float sm[];
   float *sk = sm, *sv = sk + TR * (HD + PAD);
   const Stream<HD> qd = {sv + TR * (HD + PAD)};

@@ -16,6 +16,7 @@ import torch
 from . import build as _build
 
 BF16, FP32 = 0, 1
+ZERO_UNUSED_ROWS = 0x100  # or'ed into the dtype of a packed-sequence or rotary call's params
 ROPE_AXIAL, ROPE_PACKED = 0, 1  # axial RoPE on grid coordinates / 1-D RoPE on the packed index
 OK, ERR_ARG, ERR_COORDS, ERR_CUDA, ERR_TIMEOUT, ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5
 ERR_LENGTHS = -6
@@ -480,7 +481,8 @@ class Pack3D:
 # ---- packed sequences: dense attention and rotary positions ------------------------------
 
 _DTYPES = {"bf16": BF16, "fp32": FP32, torch.bfloat16: BF16, torch.float32: FP32}
-_TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32}
+_TORCH_DTYPE = {BF16: torch.bfloat16, FP32: torch.float32,
+                BF16 | ZERO_UNUSED_ROWS: torch.bfloat16, FP32 | ZERO_UNUSED_ROWS: torch.float32}
 
 
 def make_seq_params(n_seqs: int, n_tokens: int, heads: int, kv_heads: int = None,
@@ -571,10 +573,13 @@ class _Launch:
             raise ValueError(f"{what} must be a contiguous {dtype} tensor {tuple(shape)} on "
                              f"cuda:{self.index}")
 
-    def like(self, t, shape):
+    def like(self, t, shape, zero):
         """An empty tensor without gaps in the shape and type of t (the quickest way
-        to one: the smallest calls spend most of their time on the host)."""
-        return self.kept(torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape))
+        to one: the smallest calls spend most of their time on the host).  Its rows of
+        no sequence must not stay what the memory held: the call zeroes them when all
+        its outputs are new, and `zero` is for the others."""
+        t = self.kept(torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape))
+        return t.zero_() if zero else t
 
     def kept(self, t):
         if self.given is not None:
@@ -635,6 +640,13 @@ def pack3d_seq_index_check(index: SeqIndex, stream=None) -> int:
         return int(load().pack3d_seq_index_check(index.struct, at.raw))
 
 
+def _zeroing(params):
+    """The params of a call that zeroes its outputs' rows of no sequence."""
+    p = SeqParams.from_buffer_copy(params)
+    p.dtype = params.dtype | ZERO_UNUSED_ROWS
+    return p
+
+
 def _seq_call(params, index, at):
     if index.device != at.index:
         raise ValueError(f"the index is on cuda:{index.device}, not on cuda:{at.index}")
@@ -646,19 +658,30 @@ def pack3d_seq_forward(params: SeqParams, index: SeqIndex, q, k, v, out=None, ls
                        stream=None):
     """Attention over every sequence of the pack: (out, lse).  q, k, v may be
     slices of one tensor (any token stride that is a multiple of 8 elements).
-    Rows behind the last sequence are left as they were."""
+    Rows behind the last sequence are left as they were in a given out or lse, and
+    zero in a new one."""
     with _Launch(q, stream) as at:
         qs, ks, ls, dt = _seq_call(params, index, at)
-        st = SeqStrides(q=at.rows(q, qs, dt, "q"), k=at.rows(k, ks, dt, "k"),
-                        v=at.rows(v, ks, dt, "v"))
+        st = SeqStrides()
+        if s := at.rows(q, qs, dt, "q"):  # (a structure's field costs host time)
+            st.q = s
+        if s := at.rows(k, ks, dt, "k"):
+            st.k = s
+        if s := at.rows(v, ks, dt, "v"):
+            st.v = s
+        new = out is None and lse is None
         if out is None:
-            out = at.like(q, qs)
+            out = at.like(q, qs, not new)
         else:
             st.out = at.rows(out, qs, dt, "out")
         if lse is None:
             lse = at.kept(q.new_empty(ls, dtype=torch.float32))
+            if not new:
+                lse.zero_()
         else:
             at.flat(lse, ls, torch.float32, "lse")
+        if new:
+            params = _zeroing(params)
         _check(load().pack3d_seq_forward(params, index.struct, st, q.data_ptr(), k.data_ptr(),
                                          v.data_ptr(), out.data_ptr(), lse.data_ptr(), at.raw),
                "pack3d_seq_forward")
@@ -671,25 +694,37 @@ def pack3d_seq_backward_workspace_bytes(params: SeqParams) -> int:
 
 def pack3d_seq_backward(params: SeqParams, index: SeqIndex, q, k, v, out, lse, dout, dq=None,
                         dk=None, dv=None, workspace=None, stream=None):
-    """Gradients (dq, dk, dv) from the forward's out and lse."""
+    """Gradients (dq, dk, dv) from the forward's out and lse.  Rows behind the last
+    sequence are left as they were in a given gradient, and zero in a new one."""
     with _Launch(q, stream) as at:
         qs, ks, ls, dt = _seq_call(params, index, at)
-        st = SeqStrides(q=at.rows(q, qs, dt, "q"), k=at.rows(k, ks, dt, "k"),
-                        v=at.rows(v, ks, dt, "v"), out=at.rows(out, qs, dt, "out"),
-                        dout=at.rows(dout, qs, dt, "dout"))
+        st = SeqStrides()
+        if s := at.rows(q, qs, dt, "q"):
+            st.q = s
+        if s := at.rows(k, ks, dt, "k"):
+            st.k = s
+        if s := at.rows(v, ks, dt, "v"):
+            st.v = s
+        if s := at.rows(out, qs, dt, "out"):
+            st.out = s
+        if s := at.rows(dout, qs, dt, "dout"):
+            st.dout = s
         at.flat(lse, ls, torch.float32, "lse")
+        new = dq is None and dk is None and dv is None
         if dq is None:
-            dq = at.like(q, qs)
+            dq = at.like(q, qs, not new)
         else:
             st.dq = at.rows(dq, qs, dt, "dq")
         if dk is None:
-            dk = at.like(k, ks)
+            dk = at.like(k, ks, not new)
         else:
             st.dk = at.rows(dk, ks, dt, "dk")
         if dv is None:
-            dv = at.like(v, ks)
+            dv = at.like(v, ks, not new)
         else:
             st.dv = at.rows(dv, ks, dt, "dv")
+        if new:
+            params = _zeroing(params)
         if workspace is None:
             workspace = at.kept(q.new_empty(pack3d_seq_backward_workspace_bytes(params),
                                             dtype=torch.uint8))
@@ -714,15 +749,18 @@ def _rotary(name, params, positions, q, k, q_out, k_out, stream):
         p = RotaryParams.from_buffer_copy(params)
         p.n_tokens, p.Hq, p.Hk = n, q.shape[1], 0
         p.stride_q = at.rows(q, qs, dt, "q")
+        new = q_out is None and (k is None or k_out is None)
+        if new:
+            p.dtype |= ZERO_UNUSED_ROWS
         if q_out is None:
-            q_out = at.like(q, qs)
+            q_out = at.like(q, qs, not new)
         else:
             p.stride_q_out = at.rows(q_out, qs, dt, "q_out")
         if k is not None:
             ks = (n, k.shape[1], d)
             p.Hk, p.stride_k = k.shape[1], at.rows(k, ks, dt, "k")
             if k_out is None:
-                k_out = at.like(k, ks)
+                k_out = at.like(k, ks, not new)
             else:
                 p.stride_k_out = at.rows(k_out, ks, dt, "k_out")
         _check(getattr(load(), name)(p, positions.data_ptr(), q.data_ptr(),
@@ -735,7 +773,8 @@ def pack3d_rotary(params: RotaryParams, positions, q, k=None, q_out=None, k_out=
                   stream=None):
     """Turn q [rows, heads, head_dim] and k by their rows' positions (int32);
     returns q_out, or (q_out, k_out) with k.  ``q_out=q, k_out=k`` turns them in
-    place.  Rows with a negative position are left as they were."""
+    place.  Rows with a negative position are left as they were in a given output,
+    and zero in a new one."""
     return _rotary("pack3d_rotary", params, positions, q, k, q_out, k_out, stream)
 
 
@@ -747,7 +786,8 @@ def pack3d_rotary_backward(params: RotaryParams, positions, dq_out, dk_out=None,
 
 class SeqAttention:
     """Convenience wrapper: one pack shape, its index, and the calls; ``rotary``
-    (RotaryParams) turns q and k by their positions in their sequences first."""
+    (RotaryParams) turns q and k by their positions in their sequences first.  Rows
+    behind the last sequence are zero in every tensor that it makes."""
 
     def __init__(self, params: SeqParams, rotary: RotaryParams = None):
         self.params, self.rotary, self.index = params, rotary, None

@@ -1,0 +1,140 @@
+"""Calls of the packed-sequence operators that a user may make beside the plain ones:
+padded packs, several packs in flight, an index that holds an error, logits that move
+the running maximum."""
+import pytest
+import torch
+
+import seq_common as S
+from local_global_attention_b200 import pack3d as P
+
+pytestmark = pytest.mark.gpu
+
+
+def built(lens, heads, kv_heads, dim, causal, dtype, tail=0, scale=0.0):
+    p = P.make_seq_params(len(lens), sum(lens) + tail, heads, kv_heads, dim, causal, dtype, scale)
+    cu = torch.tensor(S.prefix(lens), dtype=torch.int32, device="cuda")
+    ix = P.pack3d_seq_build_index(p, cu)
+    assert P.pack3d_seq_index_check(ix) == P.OK
+    return p, ix
+
+
+# ---- rows behind the last sequence ---------------------------------------------------------
+
+
+def dirty(shapes):
+    """Leave NaN in memory that the next tensors of these shapes and types get."""
+    kept = [torch.full(s, float("nan"), dtype=t, device="cuda") for s, t in shapes for _ in range(3)]
+    del kept
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,tail", [([100, 0, 190], 37), ([0], 5), ([128], 1), ([256, 256], 256),
+                                       ([1] * 40, 900), ([700, 3], 130), ([5], 1111)], ids=str)
+@pytest.mark.parametrize("dim,causal,layout", [(48, True, "half"), (96, False, "interleaved"),
+                                               (128, True, "interleaved"), (72, False, "half")])
+def test_new_outputs_are_zero_behind_the_last_sequence(lens, tail, dim, causal, layout, dtype):
+    """Memory that held NaN before: a padded pack's weight gradients x^T dq would hold
+    them too."""
+    H, K, n = 4, 2, sum(lens)
+    op = P.SeqAttention(P.make_seq_params(len(lens), n + tail, H, K, dim, causal, dtype),
+                        P.make_rotary_params(dim, dim // 8 * 4, layout, dtype=dtype))
+    op.build_index(torch.tensor(S.prefix(lens), dtype=torch.int32, device="cuda"))
+    q, k, v, dout = S.make(lens, H, K, dim, dtype, 3, False, tail)
+    for x in (q, k, v, dout):
+        x[n:] = float("nan")
+    shapes = [(q.shape, q.dtype), (k.shape, k.dtype), ((H, n + tail), torch.float32)]
+    dirty(shapes)
+    out, lse, rot = op.forward(q, k, v)
+    dirty(shapes)
+    grads = op.backward(rot, v, out, lse, dout)
+    for x in (out, *rot, *grads):
+        assert not x[n:].any() and torch.isfinite(x).all()
+    assert not lse[:, n:].any() and torch.isfinite(lse).all()
+    # the same rows as without the padding
+    p, ix = built(lens, H, K, dim, causal, dtype)
+    if n:
+        part = [x[:n].contiguous() for x in (*rot, v, dout)]
+        o, z = P.pack3d_seq_forward(p, ix, *part[:3])
+        assert torch.equal(o, out[:n]) and torch.equal(z, lse[:, :n])
+        g = P.pack3d_seq_backward(p, ix, *part[:3], o, z, part[3])
+        assert torch.equal(g[2], grads[2][:n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_given_and_new_outputs_of_one_call(dtype):
+    """Given outputs keep their rows behind the last sequence, new ones beside them are
+    zero there."""
+    lens, tail, H, K, d = [130, 61], 70, 2, 1, 64
+    n, N = sum(lens), sum(lens) + tail
+    p, ix = built(lens, H, K, d, True, dtype, tail)
+    q, k, v, dout = S.make(lens, H, K, d, dtype, 4, False, tail)
+    want = P.pack3d_seq_forward(p, ix, q, k, v)
+    wg = P.pack3d_seq_backward(p, ix, q, k, v, *want, dout)
+    shapes = [(q.shape, q.dtype), (k.shape, k.dtype), ((H, N), torch.float32)]
+
+    def same(got, kept, want, rows):
+        a, b = (got, want) if rows == 0 else (got.T, want.T)
+        assert torch.equal(a[:n], b[:n])
+        assert (a[n:] == (7 if kept else 0)).all()
+
+    for given in ((True, False), (False, True), (True, True)):
+        o = torch.full_like(q, 7) if given[0] else None
+        z = torch.full((H, N), 7.0, device="cuda") if given[1] else None
+        dirty(shapes)
+        got = P.pack3d_seq_forward(p, ix, q, k, v, o, z)
+        same(got[0], given[0], want[0], 0)
+        same(got[1], given[1], want[1], 1)
+    for one in range(3):
+        outs = [torch.full_like(x, 7) if i == one else None for i, x in enumerate((q, k, v))]
+        dirty(shapes)
+        got = P.pack3d_seq_backward(p, ix, q, k, v, *want, dout, *outs)
+        for i in range(3):
+            same(got[i], i == one, wg[i], 0)
+    pos = ix.positions
+    r = P.make_rotary_params(d, 48, dtype=dtype)
+    wq, wk = P.pack3d_rotary(r, pos, q, k)
+    dirty(shapes)
+    qo, ko = P.pack3d_rotary(r, pos, q, k, q_out=torch.full_like(q, 7))
+    same(qo, True, wq, 0)
+    same(ko, False, wk, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_zeroed_rows_in_strided_outputs_and_in_place(dtype):
+    """The C calls with the flag: rows of no sequence of given slices become zero, what
+    stands between the slices stays."""
+    lens, tail, H, K, d = [150, 9], 41, 3, 1, 40
+    n, N = sum(lens), sum(lens) + tail
+    p, ix = built(lens, H, K, d, False, dtype, tail)
+    q, k, v, dout = S.make(lens, H, K, d, dtype, 6, True, tail)
+    want = P.pack3d_seq_forward(p, ix, q, k, v)
+    wg = P.pack3d_seq_backward(p, ix, q, k, v, *want, dout)
+    p.dtype |= P.ZERO_UNUSED_ROWS
+    wide = torch.full((N, H + 2 * K + 1, d), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((H, N), 7.0, device="cuda")
+    P.pack3d_seq_forward(p, ix, q, k, v, wide[:, 1:1 + H], lse)
+    assert torch.equal(wide[:, 1:1 + H], want[0]) and torch.equal(lse, want[1])
+    assert (wide[:, 0] == 7).all() and (wide[:, 1 + H:] == 7).all()
+    wide[:] = 7
+    P.pack3d_seq_backward(p, ix, q, k, v, *want, dout, wide[:, 1:1 + H], wide[:, 1 + H:1 + H + K],
+                          wide[:, 1 + H + K:])
+    assert torch.equal(wide[:, 1:], torch.cat(wg, 1)) and (wide[:, 0] == 7).all()
+    # rotary in place, part of the head
+    r = P.make_rotary_params(d, 24, dtype=dtype)
+    wq, wk = P.pack3d_rotary(r, ix.positions, q, k)
+    r.dtype |= P.ZERO_UNUSED_ROWS
+    q2, k2 = q.clone(), k.clone()
+    P.pack3d_rotary(r, ix.positions, q2, k2, q2, k2)
+    assert torch.equal(q2, wq) and torch.equal(k2, wk) and not q2[n:].any()
+
+
+def test_rows_of_an_index_that_was_never_built():
+    """It holds no sequence: every row of a new output is one of no sequence."""
+    p = P.make_seq_params(2, 300, 2, 1, 64, True, "bf16")
+    ix = P.SeqIndex(p)
+    q, k, v, dout = S.make([300], 2, 1, 64, "bf16")
+    dirty([(q.shape, q.dtype), (k.shape, k.dtype), ((2, 300), torch.float32)])
+    out, lse = P.pack3d_seq_forward(p, ix, q, k, v)
+    assert not out.any() and not lse.any()
+    dirty([(q.shape, q.dtype), (k.shape, k.dtype)])
+    assert not any(x.any() for x in P.pack3d_seq_backward(p, ix, q, k, v, out, lse, dout))
