@@ -600,6 +600,7 @@ class SeqIndex:
         self.buffer = torch.zeros(nbytes + 256, dtype=torch.uint8, device=device or "cuda")
         self.device = self.buffer.get_device()
         self.struct = SeqIndexStruct()
+        self.builds = 0  # calls that built it: what a forward's index held when it ran
         base = self.buffer.data_ptr()
         _check(lib.pack3d_seq_index_init(ctypes.byref(params), base + (-base) % 256, nbytes,
                                          ctypes.byref(self.struct)), "pack3d_seq_index_init")
@@ -631,6 +632,7 @@ def pack3d_seq_build_index(params: SeqParams, cu_seqlens: torch.Tensor, index: S
             raise ValueError(f"the index is on cuda:{index.device}, not on cuda:{at.index}")
         _check(load().pack3d_seq_build_index(params, cu_seqlens.data_ptr(), index.struct, at.raw),
                "pack3d_seq_build_index")
+        index.builds += 1
     return index
 
 
@@ -784,10 +786,20 @@ def pack3d_rotary_backward(params: RotaryParams, positions, dq_out, dk_out=None,
     return _rotary("pack3d_rotary_backward", params, positions, dq_out, dk_out, dq, dk, stream)
 
 
+class _Rotated(tuple):
+    """A forward's (q, k) at their positions, with the index it ran with and that
+    index's count of builds."""
+
+
 class SeqAttention:
     """Convenience wrapper: one pack shape, its index, and the calls; ``rotary``
     (RotaryParams) turns q and k by their positions in their sequences first.  Rows
-    behind the last sequence are zero in every tensor that it makes."""
+    behind the last sequence are zero in every tensor that it makes.
+
+    ``build_index`` rebuilds the wrapper's index in place (a captured graph then
+    follows the new lengths).  Packs in flight at once, such as micro-batches whose
+    backwards run later, each need an index of their own: one of
+    ``pack3d_seq_build_index(op.params, cu_seqlens)``, given to ``forward``."""
 
     def __init__(self, params: SeqParams, rotary: RotaryParams = None):
         self.params, self.rotary, self.index = params, rotary, None
@@ -798,21 +810,37 @@ class SeqAttention:
             _check(pack3d_seq_index_check(self.index, stream), "pack3d_seq_index_check")
         return self.index
 
-    def rotate(self, q, k, stream=None):
+    def rotate(self, q, k, stream=None, index=None):
         """q and k at their positions (as they are without ``rotary``)."""
         if self.rotary is None:
             return q, k
-        return pack3d_rotary(self.rotary, self.index.positions, q, k, stream=stream)
+        index = self.index if index is None else index
+        return pack3d_rotary(self.rotary, index.positions, q, k, stream=stream)
 
-    def forward(self, q, k, v, stream=None):
-        """(out, lse, (q, k) at their positions, which the backward takes)."""
-        qr, kr = self.rotate(q, k, stream)
-        return (*pack3d_seq_forward(self.params, self.index, qr, kr, v, stream=stream), (qr, kr))
+    def forward(self, q, k, v, stream=None, index=None):
+        """(out, lse, (q, k) at their positions, which the backward takes), with the
+        wrapper's index or the given one."""
+        index = self.index if index is None else index
+        rotated = _Rotated(self.rotate(q, k, stream, index))
+        rotated.index, rotated.builds = index, index.builds
+        return (*pack3d_seq_forward(self.params, index, *rotated, v, stream=stream), rotated)
 
-    def backward(self, rotated, v, out, lse, dout, stream=None):
+    def backward(self, rotated, v, out, lse, dout, stream=None, index=None):
+        """(dq, dk, dv) with the index of the forward that gave ``rotated``; ValueError
+        if that index has been built anew since.  For a plain pair (q, k): with the
+        given index, or the wrapper's."""
+        if isinstance(rotated, _Rotated):
+            if index is not None and index is not rotated.index:
+                raise ValueError("the forward ran with another index")
+            index = rotated.index
+            if index.builds != rotated.builds:
+                raise ValueError("the index was built anew after the forward: its sequences may "
+                                 "not be the forward's (give each pack in flight its own index)")
+        elif index is None:
+            index = self.index
         qr, kr = rotated
-        dq, dk, dv = pack3d_seq_backward(self.params, self.index, qr, kr, v, out, lse, dout,
+        dq, dk, dv = pack3d_seq_backward(self.params, index, qr, kr, v, out, lse, dout,
                                          stream=stream)
         if self.rotary is not None:
-            pack3d_rotary_backward(self.rotary, self.index.positions, dq, dk, dq, dk, stream)
+            pack3d_rotary_backward(self.rotary, index.positions, dq, dk, dq, dk, stream)
         return dq, dk, dv

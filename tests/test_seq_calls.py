@@ -32,3 +32,30 @@ def test_zeroing_flag_is_no_type(lib):
         p.dtype = r.dtype = bad
         assert lib.pack3d_seq_index_bytes(p) == 0
         assert lib.pack3d_rotary(r, *[None] * 6) == P.ERR_ARG
+
+
+def test_wrapper_keeps_a_forward_with_its_index(monkeypatch):
+    """SeqAttention's bookkeeping, with the calls beneath it replaced: the backward runs
+    with its forward's index, and not once that has been built anew."""
+    class Index:
+        builds, positions = 1, None
+
+    seen = []
+    monkeypatch.setattr(P, "pack3d_seq_forward", lambda p, ix, q, k, v, stream: ("out", "lse"))
+    monkeypatch.setattr(P, "pack3d_seq_backward", lambda p, ix, *a, stream: seen.append(ix) or a[:3])
+    op, own, other = P.SeqAttention(None), Index(), Index()
+    op.index = own
+    first = op.forward("q", "k", "v")
+    second = op.forward("q", "k", "v", index=other)
+    assert first[2] == ("q", "k")
+    op.backward(second[2], "v", "out", "lse", "dout")
+    op.backward(first[2], "v", "out", "lse", "dout")
+    assert seen == [other, own]
+    own.builds += 1
+    with pytest.raises(ValueError):
+        op.backward(first[2], "v", "out", "lse", "dout")
+    with pytest.raises(ValueError):
+        op.backward(second[2], "v", "out", "lse", "dout", index=own)
+    op.backward(second[2], "v", "out", "lse", "dout", index=other)
+    op.backward(("q", "k"), "v", "out", "lse", "dout")
+    assert seen[2:] == [other, own]

@@ -138,3 +138,91 @@ def test_rows_of_an_index_that_was_never_built():
     assert not out.any() and not lse.any()
     dirty([(q.shape, q.dtype), (k.shape, k.dtype)])
     assert not any(x.any() for x in P.pack3d_seq_backward(p, ix, q, k, v, out, lse, dout))
+
+
+# ---- several packs in flight ---------------------------------------------------------------
+
+
+def layer(lens, dtype="bf16"):
+    H, K, d = 4, 2, 64
+    op = P.SeqAttention(P.make_seq_params(len(lens), sum(lens), H, K, d, True, dtype),
+                        P.make_rotary_params(d, dtype=dtype))
+    return op, [torch.tensor(S.prefix(x), dtype=torch.int32, device="cuda")
+                for x in (lens, lens[::-1])]
+
+
+def test_backward_after_another_pack_was_built():
+    """The wrapper's index holds the lengths of the last pack: the backward of the pack
+    before it is refused."""
+    lens = [100, 300, 17]
+    op, (a, b) = layer(lens)
+    q, k, v, dout = S.make(lens, 4, 2, 64, "bf16", 1)
+    op.build_index(a)
+    out, lse, rot = op.forward(q, k, v)
+    want = op.backward(rot, v, out, lse, dout)
+    op.build_index(b)
+    with pytest.raises(ValueError):
+        op.backward(rot, v, out, lse, dout)
+    with pytest.raises(ValueError):
+        op.backward(rot, v, out, lse, dout, index=P.pack3d_seq_build_index(op.params, a))
+    out, lse, rot = op.forward(q, k, v)  # the pack that the index holds
+    op.backward(rot, v, out, lse, dout)
+    # a plain pair goes with the given index
+    op.build_index(a)
+    out, lse, rot = op.forward(q, k, v)
+    for index in (None, P.pack3d_seq_build_index(op.params, a)):
+        got = op.backward(tuple(rot), v, out, lse, dout, index=index)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_packs_in_flight_with_their_own_indexes():
+    """Two micro-batches: both forwards, then both backwards."""
+    lens = [100, 300, 17]
+    op, cus = layer(lens)
+    sets = [S.make(lens, 4, 2, 64, "bf16", s) for s in (1, 2)]
+    want = []
+    for cu, (q, k, v, dout) in zip(cus, sets):
+        op.build_index(cu)
+        out, lse, rot = op.forward(q, k, v)
+        want.append((out, lse, *op.backward(rot, v, out, lse, dout)))
+    idx = [P.pack3d_seq_build_index(op.params, cu) for cu in cus]
+    runs = [op.forward(*x[:3], index=ix) for x, ix in zip(sets, idx)]
+    for (out, lse, rot), x, w in zip(runs, sets, want):
+        got = (out, lse, *op.backward(rot, x[2], out, lse, x[3]))
+        assert all(torch.equal(m, n) for m, n in zip(got, w))
+
+
+def test_wrapper_in_a_graph_follows_the_lengths():
+    """Index, forward and backward of one captured step, replayed with other lengths
+    written into its prefix sums; and an index built anew outside a graph that holds the
+    forward alone."""
+    lens = [100, 300, 17]
+    op, (a, b) = layer(lens)
+    q, k, v, dout = S.make(lens, 4, 2, 64, "bf16", 1)
+
+    def step():
+        out, lse, rot = op.forward(q, k, v)
+        return (out, lse, *op.backward(rot, v, out, lse, dout))
+
+    want = []
+    for cu in (a, b):
+        op.build_index(cu)
+        want.append(step())
+    cu = a.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.build_index(cu, check=False)
+        res = step()
+    for x, w in ((b, want[1]), (a, want[0])):
+        cu.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for m, n in zip(res, w))
+    alone = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(alone):
+        res = step()
+    for x, w in ((b, want[1]), (a, want[0])):
+        op.build_index(x)
+        alone.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, n) for m, n in zip(res, w))
