@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(NT, 1)
   const Tile t = load_tile_entry(ix.query, blockIdx.x / g.Hq);
   const int64_t window = (int64_t)(blockIdx.x / g.Hq) * ROWS;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   if (unused_rows(g, now.rows, window, ROWS))
     zero_unused(g, now.rows, window, ROWS, dq + (int64_t)h * g.d, st.dq);
   if (t.len == 0) return;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(NT, 1)
   const Tile t = load_tile_entry(ix.key, blockIdx.x / g.Hk);
   const int64_t window = (int64_t)(blockIdx.x / g.Hk) * ROWS;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   if (unused_rows(g, now.rows, window, ROWS)) {
     zero_unused(g, now.rows, window, ROWS, dk + (int64_t)hk * g.d, st.dk);
     zero_unused(g, now.rows, window, ROWS, dv + (int64_t)hk * g.d, st.dv);

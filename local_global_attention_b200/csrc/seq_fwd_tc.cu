@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(NT, 1)
   const Tile t = load_tile_entry(ix.pair, blockIdx.x / g.Hq);
   const int64_t window = (int64_t)(blockIdx.x / g.Hq) * PAIR;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   if (unused_rows(g, now.rows, window, PAIR)) {
     zero_unused(g, now.rows, window, PAIR, out + (int64_t)h * g.d, stride_out);
     const int64_t row = window + threadIdx.x;

@@ -46,13 +46,21 @@ __device__ __forceinline__ Tile load_tile_entry(const int32_t* list, int i) {
   return Tile{x.x, x.y, x.z, x.w};
 }
 
-// The index's error word and the rows that its sequences hold (cu[n_seqs]).
+// The index's error word and the rows that its sequences hold (cu[n_seqs]).  A block
+// decides once whether the index holds an error: another block, of this launch or of
+// one on another stream, may set the timeout bit between the loads of two warps, and
+// warps that went on without those that left would wait on barriers and use tensor
+// memory that nobody has set up.  (The barrier takes 0.1 us of a kernel's 6 to 9.)
 struct State {
   int err, rows;
 };
 __device__ __forceinline__ State load_state(const pack3d_seq_index& ix) {
   const int2 x = *reinterpret_cast<const int2*>(ix.err);
   return State{x.x, x.y};
+}
+
+__device__ __forceinline__ bool block_failed(const State& now) {
+  return __syncthreads_or(now.err) != 0;
 }
 
 // Zeros into those of the rows [first, first + n) of one head that belong to no

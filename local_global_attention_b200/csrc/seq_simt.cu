@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(NT)
   Tile t;
   int off, rows;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   const int64_t window = (int64_t)blockIdx.x * TR;
   if (unused_rows(g, now.rows, window, TR)) {
     zero_unused(g, now.rows, window, TR, out + (int64_t)blockIdx.y * g.d, st.out);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(NT)
   Tile t;
   int off, rows;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   const int64_t window = (int64_t)blockIdx.x * TR;
   if (unused_rows(g, now.rows, window, TR))
     zero_unused(g, now.rows, window, TR, dq + (int64_t)blockIdx.y * g.d, st.dq);
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(NT)
   Tile t;
   int off, rows;
   const State now = load_state(ix);
-  if (now.err) return;
+  if (block_failed(now)) return;
   const int64_t window = (int64_t)blockIdx.x * TR;
   if (unused_rows(g, now.rows, window, TR)) {
     zero_unused(g, now.rows, window, TR, dk + (int64_t)blockIdx.y * g.d, st.dk);

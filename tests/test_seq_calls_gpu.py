@@ -226,3 +226,34 @@ def test_wrapper_in_a_graph_follows_the_lengths():
         alone.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(m, n) for m, n in zip(res, w))
+
+
+# ---- an index that holds an error ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [64, 96, 128])
+def test_index_with_the_timeout_bit(dim, dtype):
+    """The bit that a kernel sets when a bounded wait gives up, written here by the host:
+    later calls write nothing, the check reports it, building anew clears it."""
+    lens, H, K = [300, 129], 4, 2
+    p, ix = built(lens, H, K, dim, True, dtype, 11)
+    q, k, v, dout = S.make(lens, H, K, dim, dtype, 2, False, 11)
+    want = P.pack3d_seq_forward(p, ix, q, k, v)
+    off = ix.struct.err - ix.buffer.data_ptr()
+    err = ix.buffer[off:off + 8].view(torch.int32)
+    assert err.tolist() == [0, sum(lens)]
+    err[0] = 4
+    assert P.pack3d_seq_index_check(ix) == P.ERR_TIMEOUT
+    kept = [torch.full_like(x, 7) for x in (q, q, k, v)]
+    lse = torch.full_like(want[1], 7)
+    p.dtype |= P.ZERO_UNUSED_ROWS
+    P.pack3d_seq_forward(p, ix, q, k, v, kept[0], lse)
+    P.pack3d_seq_backward(p, ix, q, k, v, *want, dout, *kept[1:])
+    assert all((x == 7).all() for x in (*kept, lse))
+    assert P.pack3d_seq_index_check(ix) == P.ERR_TIMEOUT
+    cu = torch.tensor(S.prefix(lens), dtype=torch.int32, device="cuda")
+    P.pack3d_seq_build_index(p, cu, ix)
+    assert P.pack3d_seq_index_check(ix) == P.OK
+    got = P.pack3d_seq_forward(p, ix, q, k, v)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
