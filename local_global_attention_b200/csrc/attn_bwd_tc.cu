@@ -205,7 +205,7 @@ __device__ __forceinline__ void load_acc_row(uint32_t taddr, float (&v)[96]) {
 template <int ROLE, bool PARTIAL>
 __global__ void __launch_bounds__(NTHREADS, 1)
     k_bwd_tc(Geo g, pack3d_index ix, const __grid_constant__ BwdMaps maps, BwdArgs args) {
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(256)
                   const float* __restrict__ lse, __nv_bfloat16* __restrict__ qg,
                   __nv_bfloat16* __restrict__ dog, float4* __restrict__ stat,
                   uint4* __restrict__ schan) {
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   __shared__ int32_t tok[STAGE_XS];
   // delta partials: per (voxel, head of the group) the dot products of the six items
   __shared__ float part[STAGE_XS][STAGE_HG][6];

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(TILE * Split<D>::G) k_forward_simt(
     const T* __restrict__ v, const float* __restrict__ ksum, const float* __restrict__ vsum,
     TO* __restrict__ out, float* __restrict__ lse) {
   constexpr int G = Split<D>::G, CPT = Split<D>::CPT;
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   __shared__ float sk[KC][D];
   __shared__ float sv[KC][D];
   __shared__ ChunkCoords cc;
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) k_bwd_summary(Geo g, pack3d_index ix,
                                                     const float* __restrict__ ksum,
                                                     const float* __restrict__ vsum, float* dks,
                                                     float* dvs) {
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   // rows padded to D + 1 floats: the dot products read rows kk of skb / svb at
   // the same channel from 8 threads, which would otherwise share a bank
   __shared__ float sq[QC][D + 1];
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(S96_THREADS, 2) k_bwd_summary96(
     const float* __restrict__ ksum, const float* __restrict__ vsum, int nsplit,
     float* __restrict__ part) {
   constexpr int D = 96;
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   extern __shared__ __align__(16) unsigned char s96_raw[];
   Sum96Smem& sm = *reinterpret_cast<Sum96Smem*>(s96_raw);
   const int nbc = (g.nb + S96_NB - 1) / S96_NB;
@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(TILE * Split<D>::G) k_bwd_dq(
     const float* __restrict__ delta, const float* __restrict__ ksum,
     const float* __restrict__ vsum, T* __restrict__ dq) {
   constexpr int G = Split<D>::G, CPT = Split<D>::CPT;
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   // dynamic: staged keys and values, 2 * CAPK rows of D floats
   extern __shared__ __align__(16) float bwd_dyn[];
   float* const sbuf = bwd_dyn;
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(TILE * Split<D>::G) k_bwd_dkdv(
     const float* __restrict__ delta, const float* __restrict__ dks,
     const float* __restrict__ dvs, T* __restrict__ dk, T* __restrict__ dv) {
   constexpr int G = Split<D>::G, CPT = Split<D>::CPT;
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   // dynamic: staged queries and dO rows, 2 * CAPK rows of D floats
   extern __shared__ __align__(16) float bwd_dyn[];
   float* const sbuf = bwd_dyn;

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256)
     k_grid_kv(Geo g, pack3d_index ix, const __nv_bfloat16* __restrict__ k,
               const __nv_bfloat16* __restrict__ v, __nv_bfloat16* __restrict__ kg,
               __nv_bfloat16* __restrict__ vg) {
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   __shared__ int32_t tok[GRID_XS];
   const int xb = blockIdx.x * GRID_XS, zy = blockIdx.y, b = blockIdx.z;
   const int z = zy / g.Y, y = zy % g.Y;
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(NTHREADS, 2)
     k_forward_tc(Geo g, pack3d_index ix, const __nv_bfloat16* __restrict__ q,
                  const __grid_constant__ Maps maps, void* __restrict__ out_raw,
                  float* __restrict__ lse) {
-  if (ix.err[0]) return;
+  if (block_failed(ix.err)) return;
   extern __shared__ uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                       ~(uintptr_t)1023);

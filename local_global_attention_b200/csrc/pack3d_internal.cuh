@@ -60,6 +60,14 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// Whether the index holds an error, decided once for the block (in kernels with block
+// barriers): a block of this launch, or of one on another stream, may set the timeout
+// bit between the loads of two warps, and warps that went on without those that left
+// would use barriers and shared memory that nobody has set up.
+__device__ __forceinline__ bool block_failed(const int32_t* err) {
+  return __syncthreads_or(err[0]) != 0;
+}
+
 // Whether voxel (z, y, x) of batch item b holds a token: always in a dense
 // volume; else the coordinate volume has its token or -1.
 __device__ __forceinline__ bool occupied(const Geo& g, const int32_t* vol, int b, int z, int y,

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(256) k_block_summaries(Geo g, const int32_t* _
                                                          const T* __restrict__ k,
                                                          const T* __restrict__ v, float* ksum,
                                                          float* vsum) {
-  if (err[0]) return;
+  if (block_failed(err)) return;
   using P2 = typename Pair2<T>::type;
   extern __shared__ float red[];  // [TG][2][d]
   const int lanes = g.d / 4;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(TG96 * LANES96) k_block_summaries_bf16_d96(
     const int32_t* __restrict__ err, const int32_t* __restrict__ bcount,
     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, float* ksum,
     float* vsum, StageOut so) {
-  if (err[0]) return;
+  if (block_failed(err)) return;
   __shared__ float red[TG96][HG96][2][96];
   __shared__ float2 tab_s[TAB96 * TABS96];
   const int u = threadIdx.x % LANES96, grp = threadIdx.x / LANES96;
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(BS_THREADS, 2) k_summaries_bulk(
     const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v, float* ksum,
     float* vsum, StageOut so) {
   using namespace tc;
-  if (err[0]) return;
+  if (block_failed(err)) return;
   extern __shared__ uint8_t bs_raw[];
   BulkSmem& sm = *reinterpret_cast<BulkSmem*>((reinterpret_cast<uintptr_t>(bs_raw) + 127) &
                                               ~(uintptr_t)127);
