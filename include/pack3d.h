@@ -515,7 +515,8 @@ typedef struct {
   int32_t n_tokens, Hq, Hk, head_dim; /* head_dim a multiple of 8, at most 256; Hk may be 0 */
   int32_t rot_dim;                    /* even, 2 .. head_dim */
   int32_t layout, dtype;              /* dtype may hold PACK3D_ZERO_UNUSED_ROWS */
-  float base;                         /* > 0 (RAMP: > 1) */
+  float base;                         /* > 0 (RAMP: > 1); below 1 the pairs turn faster: no
+                                         pair may make 16 turns per position or more */
   int32_t scaling;
   float factor;                       /* >= 1 (not read by NONE) */
   int32_t original_length;            /* BANDS, RAMP */

@@ -228,7 +228,12 @@ int launch_type(const RotArgs& a, int layout, const int32_t* pos, const void* q,
 // theta_j of the r/2 pairs, and the default amplitude of the scaling.  The powers
 // base^(-2j/r) are products of one factor in 64-bit mantissas (128 products are
 // off by 2^-57 at most), which takes a call 1 us less of host time than as many
-// powers.
+// powers.  With a base below 1 the frequencies grow, and a relative error of one is as
+// many times more of a turn: there every power is taken by itself (2^-61 relative),
+// and pairs of MAX_TURNS turns per position or more are refused, whose fraction would
+// keep too few bits (below it the angle of position 2^31 is off by 2^-26 of a turn at
+// most).
+constexpr long double MAX_TURNS = 16.0L;
 int frequencies(const pack3d_rotary_params* p, long double* theta, double* amp) {
   const long double two_pi = 6.283185307179586476925286766559L;
   const int r = p->rot_dim, half = r / 2;
@@ -238,7 +243,8 @@ int frequencies(const pack3d_rotary_params* p, long double* theta, double* amp) 
   if (p->scaling == PACK3D_ROTARY_BASE && r > 2) base *= powl(f, (long double)r / (r - 2));
   const long double step = powl(base, -2.0L / r);
   theta[0] = 1.0L;
-  for (int j = 1; j < half; ++j) theta[j] = theta[j - 1] * step;
+  for (int j = 1; j < half; ++j)
+    theta[j] = base < 1.0L ? powl(base, -2.0L * j / r) : theta[j - 1] * step;
   if (p->scaling == PACK3D_ROTARY_LINEAR)
     for (int j = 0; j < half; ++j) theta[j] /= f;
   if (p->scaling == PACK3D_ROTARY_BANDS)
@@ -260,7 +266,8 @@ int frequencies(const pack3d_rotary_params* p, long double* theta, double* amp) 
     }
     *amp = 0.1 * log((double)f) + 1.0;
   }
-  return isfinite(theta[half - 1]) ? PACK3D_OK : PACK3D_ERR_ARG;
+  // (the last pair is the fastest where the base is below 1, and at most 1 elsewhere)
+  return theta[half - 1] < MAX_TURNS * two_pi ? PACK3D_OK : PACK3D_ERR_ARG;
 }
 
 int check_params(const pack3d_rotary_params* p) {

@@ -59,3 +59,26 @@ def test_wrapper_keeps_a_forward_with_its_index(monkeypatch):
     op.backward(second[2], "v", "out", "lse", "dout", index=other)
     op.backward(("q", "k"), "v", "out", "lse", "dout")
     assert seen[2:] == [other, own]
+
+
+def rotary_status(lib, call, **kw):
+    """Status of a call without rows: the checks alone."""
+    r = P.make_rotary_params(96, **kw)
+    r.Hq = 8
+    return getattr(lib, call)(r, *[None] * 6)
+
+
+@pytest.mark.parametrize("call", ["pack3d_rotary", "pack3d_rotary_backward"])
+def test_rotary_bases(lib, call):
+    """Bases whose fastest pair makes too many turns per position to keep its angle's
+    bits are refused, and none else: the pair of base 0.01 makes 0.01^(-94/96) / (2 pi)
+    = 14.5 turns, that of 0.0085 17.0."""
+    for base in (1e-38, 1e-10, 1e-3, 0.0085):
+        assert rotary_status(lib, call, base=base) == P.ERR_ARG, base
+        assert rotary_status(lib, call, base=base, scaling="linear", factor=1.0) == P.ERR_ARG
+    for base in (0.01, 0.25, 0.999, 1.0, 1.5, 100.0, 5e5, 3e38):
+        assert rotary_status(lib, call, base=base) == P.OK, base
+    # a scaling that slows the pairs down, and a head with one pair
+    assert rotary_status(lib, call, base=1e-3, scaling="linear", factor=16.0) == P.OK
+    assert rotary_status(lib, call, base=1e-38, rot_dim=2) == P.OK
+    assert rotary_status(lib, call, base=1e-3, scaling="base", factor=1000.0) == P.OK

@@ -257,3 +257,31 @@ def test_index_with_the_timeout_bit(dim, dtype):
     assert P.pack3d_seq_index_check(ix) == P.OK
     got = P.pack3d_seq_forward(p, ix, q, k, v)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---- rotary bases below 1 ------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("base,r", [(0.010009765625, 96), (0.01953125, 64),
+                                    (0.5, 128), (0.90625, 8)])
+def test_rotary_fast_pairs_at_far_positions(base, r, layout):
+    """Pairs of up to 14.4 turns per position (bases that are floats).  Beside the roundings that rotated()
+    counts, the angle of position 2^31: 2^-61 relative of 14.5 x 2^31 turns is 2^-26 of
+    a turn, 0.9e-7; the 64-bit mantissas of the oracle are off by as much (a power, a
+    product and the reduction): 4 half steps 2^-24 of a (|x1| + |x2|) cover both."""
+    d = 128
+    g = torch.Generator().manual_seed(r)
+    q = torch.randn(64, 2, d, generator=g).cuda()
+    pos = torch.randint(0, 2 ** 31 - 1, (64,), generator=g).to(torch.int32).cuda()
+    p = P.make_rotary_params(d, r, layout, base, "fp32")
+    th, amp = S.frequencies(r, base)
+    for call, sense in ((P.pack3d_rotary, 1.0), (P.pack3d_rotary_backward, -1.0)):
+        val, bound = S.rotated(q, pos, th, amp, layout, sense)
+        x = q.double()
+        i1, i2 = (slice(0, r // 2), slice(r // 2, r)) if layout == "half" else \
+            (slice(0, r, 2), slice(1, r, 2))
+        more = 4 * 2.0 ** -24 * (x[..., i1].abs() + x[..., i2].abs())
+        bound[..., i1] += more
+        bound[..., i2] += more
+        S.within(call(p, pos, q), val, bound, f"{call.__name__} base {base}")
