@@ -397,9 +397,14 @@ PACK3D_API const char* pack3d_strerror(int status);
  * fp32 throughout.  Results do not depend on the run: no atomics enter a sum.
  *
  * Non-finite values: what stands in another sequence or behind the last one
- * never reaches a row.  Inside a causal sequence a non-finite value, gradient
- * or query of a token may also reach rows of up to 256 tokens before it (a
- * masked weight of zero times that value). */
+ * never reaches a row.  Inside a causal sequence they may also reach rows that
+ * the formulas keep apart from the token (a masked weight of zero times that
+ * value), in the token's own tile of the sequence, 128 rows counted from the
+ * sequence's first (fp32: 64), and nowhere else:
+ *   v     out and dq of rows before the token
+ *   k     dq of rows before it
+ *   q     dk of rows behind it
+ *   dout  dk and dv of rows behind it */
 
 /* Or'ed into the dtype of a packed-sequence or rotary call's params: the call
  * writes zeros to the outputs' rows that belong to no sequence (rotary: whose

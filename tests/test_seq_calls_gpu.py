@@ -285,3 +285,42 @@ def test_rotary_fast_pairs_at_far_positions(base, r, layout):
         bound[..., i1] += more
         bound[..., i2] += more
         S.within(call(p, pos, q), val, bound, f"{call.__name__} base {base}")
+
+
+# ---- non-finite values inside a causal sequence --------------------------------------------
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["q", "k", "v", "dout"])
+@pytest.mark.parametrize("dtype,tile,dim", [("bf16", 128, 64), ("bf16", 128, 96), ("bf16", 128, 128),
+                                            ("fp32", 64, 48)])
+def test_reach_of_a_non_finite_token(dtype, tile, dim, what, bad):
+    """The formulas take q_t to out, lse and dq of t and dk and dv up to t; k_t and v_t to
+    rows from t on and, by these, to every dk (k_t: and dv); dout_t to dq of t and dk and
+    dv up to t.  Beyond that only what the header lists, in the token's own tile: all
+    other values are the bits they are without it."""
+    lens, H, K = [90, 500, 40], 4, 2
+    p, ix = built(lens, H, K, dim, True, dtype)
+    s0, n = 90, 500
+    clean = S.make(lens, H, K, dim, dtype, 7)
+    names = ("out", "lse", "dq", "dk", "dv")
+
+    def run(q, k, v, dout):
+        out, lse = P.pack3d_seq_forward(p, ix, q, k, v)
+        return dict(zip(names, (out, lse.T, *P.pack3d_seq_backward(p, ix, q, k, v, out, lse, dout))))
+
+    want = run(*clean)
+    for t in (0, 30, 127, 128, 200, 383, 499):
+        x = [y.clone() for y in clean]
+        x[("q", "k", "v", "dout").index(what)][s0 + t] = bad
+        got = run(*x)
+        at, upto, since, all_, none = {t}, set(range(t + 1)), set(range(t, n)), set(range(n)), set()
+        own = set(range(t // tile * tile, min(n, (t // tile + 1) * tile)))
+        reach = {"q": dict(out=at, lse=at, dq=at, dk=upto | own, dv=upto),
+                 "k": dict(out=since, lse=since, dq=since | own, dk=all_, dv=all_),
+                 "v": dict(out=since | own, lse=none, dq=since | own, dk=all_, dv=none),
+                 "dout": dict(out=none, lse=none, dq=at, dk=upto | own, dv=upto | own)}[what]
+        for name in names:
+            other = [s0 + i for i in range(n) if i not in reach[name]]
+            rows = list(range(s0)) + other + list(range(s0 + n, sum(lens)))
+            assert torch.equal(got[name][rows], want[name][rows]), (name, t)
