@@ -607,7 +607,7 @@ class SeqIndex:
 
     def _rows(self, field):
         off = getattr(self.struct, field) - self.buffer.data_ptr()
-        return self.buffer[off:off + 4 * self.params.n_tokens].view(torch.int32)
+        return self.buffer[off:off + 4 * self.struct.n_tokens].view(torch.int32)
 
     @property
     def positions(self):

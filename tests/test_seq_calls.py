@@ -82,3 +82,14 @@ def test_rotary_bases(lib, call):
     assert rotary_status(lib, call, base=1e-3, scaling="linear", factor=16.0) == P.OK
     assert rotary_status(lib, call, base=1e-38, rot_dim=2) == P.OK
     assert rotary_status(lib, call, base=1e-3, scaling="base", factor=1000.0) == P.OK
+
+
+def test_views_of_an_index_whose_params_changed_since(lib):
+    """The views are of the rows that the buffer was sized for, whatever the caller's
+    params say by then."""
+    p = P.make_seq_params(3, 1000, 8, 2, 96)
+    ix = P.SeqIndex(p, device="cpu")
+    p.n_tokens = 5000
+    assert ix.positions.numel() == ix.sequences.numel() == 1000
+    p.n_tokens = 10
+    assert ix.positions.numel() == ix.sequences.numel() == 1000
