@@ -324,3 +324,62 @@ def test_reach_of_a_non_finite_token(dtype, tile, dim, what, bad):
             other = [s0 + i for i in range(n) if i not in reach[name]]
             rows = list(range(s0)) + other + list(range(s0 + n, sum(lens)))
             assert torch.equal(got[name][rows], want[name][rows]), (name, t)
+
+
+# ---- padded packs in graphs and on given streams -------------------------------------------
+
+
+def test_padded_pack_in_a_replayed_graph():
+    """Index, forward and backward in one graph over tensors of fixed size: rows that a
+    replay's sequences no longer hold are zero, not the replay before's."""
+    H, K, d, N = 4, 2, 96, 640
+    op = P.SeqAttention(P.make_seq_params(3, N, H, K, d), P.make_rotary_params(d))
+    q, k, v, dout = S.make([N], H, K, d, "bf16", 3)
+    cu = torch.tensor([0, 300, 500, 640], dtype=torch.int32, device="cuda")
+
+    def step():
+        out, lse, rot = op.forward(q, k, v)
+        return (out, lse.T, *rot, *op.backward(rot, v, out, lse, dout))
+
+    op.build_index(cu)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op.build_index(cu, check=False)
+        res = step()
+    for ends in ([300, 500, 640], [100, 100, 130], [1, 2, 3], [0, 0, 0], [128, 256, 639]):
+        cu.copy_(torch.tensor([0, *ends], dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in res]
+        assert P.pack3d_seq_index_check(op.index) == P.OK
+        assert all(not x[ends[-1]:].any() for x in got)
+        op.build_index(cu)
+        assert all(torch.equal(x, y) for x, y in zip(got, step()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_padded_packs_on_two_given_streams(dtype):
+    """Two packs at once, each with its index, outputs allocated on the given streams."""
+    H, K, d, lens, tail = 4, 2, 64, [200, 77], 301
+    n = sum(lens)
+    p, _ = built(lens, H, K, d, True, dtype, tail)
+    cu = torch.tensor(S.prefix(lens), dtype=torch.int32, device="cuda")
+    sets = [S.make(lens, H, K, d, dtype, s, False, tail) for s in (1, 2)]
+    want = []
+    for x in sets:
+        ix = P.pack3d_seq_build_index(p, cu)
+        out, lse = P.pack3d_seq_forward(p, ix, *x[:3])
+        want.append((out, lse, *P.pack3d_seq_backward(p, ix, *x[:3], out, lse, x[3])))
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    runs = []
+    for _ in range(3):
+        for x, s in zip(sets, streams):
+            ix = P.pack3d_seq_build_index(p, cu, stream=s)
+            out, lse = P.pack3d_seq_forward(p, ix, *x[:3], stream=s)
+            runs.append((out, lse, *P.pack3d_seq_backward(p, ix, *x[:3], out, lse, x[3], stream=s)))
+    torch.cuda.synchronize()
+    for i, got in enumerate(runs):
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))
+        assert not got[0][n:].any() and not got[2][n:].any()
