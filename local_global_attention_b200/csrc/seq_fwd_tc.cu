@@ -30,9 +30,9 @@
 // 128.  Every wait is bounded; a CTA that gives up sets the timeout bit of the
 // index's error word.
 //
-// Measured: a causal sequence of 32,768 tokens, 16 heads on 2, d 128, 3.6-3.7 ms
-// (1,180-1,210 TFLOP/s, 0.73 of the measured burst rate; at 990 W the clock falls
-// to 1.57 GHz); 16,384 tokens not causal, 8 heads, d 96, 0.88-0.98 ms.  Bound by the
+// Measured: a causal sequence of 32,768 tokens, 16 heads on 2, d 128, 3.65-3.87 ms
+// (1,140-1,200 TFLOP/s, 0.69-0.73 of the measured burst rate; at 990 W the clock falls
+// to 1.57 GHz); 16,384 tokens not causal, 8 heads, d 96, 0.97-1.01 ms.  Bound by the
 // chain S - softmax - P v of a tile (3,230 cycles a step of both tiles at d 128,
 // 2,960 at d 96, against 2,140 and 1,610 of tensor work) and, in long runs, by
 // power.  Short sequences pay about 7,000 cycles per CTA for set-up, first loads
@@ -51,7 +51,7 @@ constexpr int MMA_WARP = 8, TMA_WARP = 9, NT = 384;
 constexpr uint32_t TMEM_COLS = 512, COL_S = 0, COL_O = 256;
 constexpr float RESCALE_THRESHOLD = 8.0f;
 // P is handed to its product in two halves (whole: 920, quarters: 939 against
-// 884 us at 16,384 tokens, d 96, not causal).
+// 884 us at 16,384 tokens, d 96, not causal, on a cool GPU).
 constexpr int PARTS = 2;
 
 template <int HD>

@@ -20,8 +20,8 @@
 // stores.  Consecutive threads cover a head, then the next heads, so a warp's
 // accesses are whole rows.  VEC is the widest power of two (16 bytes at most)
 // that divides the pair segments, so odd rotated widths run with narrower
-// accesses.  Measured at 65,536 rows x 16 heads x 96 (402 MB): 77 us, 5.2 TB/s,
-// 0.80 of the copy bandwidth; with cosines per thread, shared by four heads
+// accesses.  Measured at 65,536 rows x 16 heads x 96 (402 MB): 78 us, 5.2 TB/s,
+// 0.79 of the copy bandwidth; with cosines per thread, shared by four heads
 // only, and loads after them 126 us.
 #include <math.h>
 

@@ -827,8 +827,8 @@ class SeqAttention:
 
     def backward(self, rotated, v, out, lse, dout, stream=None, index=None):
         """(dq, dk, dv) with the index of the forward that gave ``rotated``; ValueError
-        if that index has been built anew since.  For a plain pair (q, k): with the
-        given index, or the wrapper's."""
+        if a call has built that index anew since (replays of a captured build are not
+        counted).  For a plain pair (q, k): with the given index, or the wrapper's."""
         if isinstance(rotated, _Rotated):
             if index is not None and index is not rotated.index:
                 raise ValueError("the forward ran with another index")
