@@ -33,10 +33,11 @@
 // Measured: two causal sequences of 8,192 tokens, 16 heads on 4, d 128, 1.57 ms in a
 // burst of five calls (dq 0.69, dk/dv 0.87 each under the profiler; 1,230 TFLOP/s
 // issued, 880 of the five products' count), 1.62 over 30 calls and 1.79 over 300, as
-// power lowers the clock; 2,090 and 3,130 cycles per tile against 1,610 and 2,140 of tensor work (d 96:
-// 1,950 and 2,930 against 1,200 and 1,600).  Bound by the arithmetic warps: 64
-// exponentials a thread and tile keep the special-function unit busy for 1,024
-// cycles, and loads, products and stores of P and dS follow in the same warps.
+// power lowers the clock; 2,090 and 3,130 cycles per tile against 1,610 and 2,140 of
+// tensor work (d 96: 1,950 and 2,930 against 1,200 and 1,600).  Bound by the
+// arithmetic warps: 64 exponentials a thread and tile keep the special-function unit
+// busy for 1,024 cycles, and loads, products and stores of P and dS follow in the
+// same warps.
 #include <cuda.h>
 #include <math.h>
 

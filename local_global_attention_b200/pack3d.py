@@ -822,18 +822,21 @@ class SeqAttention:
         wrapper's index or the given one."""
         index = self.index if index is None else index
         rotated = _Rotated(self.rotate(q, k, stream, index))
-        rotated.index, rotated.builds = index, index.builds
+        rotated.index = index
+        # (a captured forward runs with whatever the index holds at each replay)
+        rotated.builds = None if torch.cuda.is_current_stream_capturing() else index.builds
         return (*pack3d_seq_forward(self.params, index, *rotated, v, stream=stream), rotated)
 
     def backward(self, rotated, v, out, lse, dout, stream=None, index=None):
         """(dq, dk, dv) with the index of the forward that gave ``rotated``; ValueError
-        if a call has built that index anew since (replays of a captured build are not
-        counted).  For a plain pair (q, k): with the given index, or the wrapper's."""
+        if a call has built that index anew since (not seen: replays of a captured build,
+        and builds after a captured forward, whose replays follow them).  For a plain pair
+        (q, k): with the given index, or the wrapper's."""
         if isinstance(rotated, _Rotated):
             if index is not None and index is not rotated.index:
                 raise ValueError("the forward ran with another index")
             index = rotated.index
-            if index.builds != rotated.builds:
+            if rotated.builds not in (None, index.builds):
                 raise ValueError("the index was built anew after the forward: its sequences may "
                                  "not be the forward's (give each pack in flight its own index)")
         elif index is None:

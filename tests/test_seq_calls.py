@@ -43,6 +43,8 @@ def test_wrapper_keeps_a_forward_with_its_index(monkeypatch):
     seen = []
     monkeypatch.setattr(P, "pack3d_seq_forward", lambda p, ix, q, k, v, stream: ("out", "lse"))
     monkeypatch.setattr(P, "pack3d_seq_backward", lambda p, ix, *a, stream: seen.append(ix) or a[:3])
+    capturing = [False]
+    monkeypatch.setattr(P.torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
     op, own, other = P.SeqAttention(None), Index(), Index()
     op.index = own
     first = op.forward("q", "k", "v")
@@ -59,6 +61,12 @@ def test_wrapper_keeps_a_forward_with_its_index(monkeypatch):
     op.backward(second[2], "v", "out", "lse", "dout", index=other)
     op.backward(("q", "k"), "v", "out", "lse", "dout")
     assert seen[2:] == [other, own]
+    # a captured forward follows the index
+    capturing[0] = True
+    third = op.forward("q", "k", "v")
+    own.builds += 1
+    op.backward(third[2], "v", "out", "lse", "dout")
+    assert seen[4:] == [own]
 
 
 def rotary_status(lib, call, **kw):

@@ -383,3 +383,24 @@ def test_padded_packs_on_two_given_streams(dtype):
     for i, got in enumerate(runs):
         assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2]))
         assert not got[0][n:].any() and not got[2][n:].any()
+
+
+def test_replayed_forward_and_eager_backward():
+    """A captured forward, replayed after the index was built for other lengths, with the
+    backward called outside the graph each time."""
+    lens = [100, 300, 17]
+    op, cus = layer(lens)
+    q, k, v, dout = S.make(lens, 4, 2, 64, "bf16", 1)
+    want = []
+    for cu in cus:
+        op.build_index(cu)
+        out, lse, rot = op.forward(q, k, v)
+        want.append((out, lse, *op.backward(rot, v, out, lse, dout)))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse, rot = op.forward(q, k, v)
+    for cu, w in zip(cus, want):
+        op.build_index(cu)
+        graph.replay()
+        got = (out, lse, *op.backward(rot, v, out, lse, dout))
+        assert all(torch.equal(x, y) for x, y in zip(got, w))
